@@ -325,6 +325,143 @@ moe_status_t moe_fc2_combine_tiled(const uint8_t* hq, const uint8_t* hs, int T, 
                                    int64_t ld_out, void* workspace, size_t ws_bytes,
                                    hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the experts: what one MoE block runs between the residual stream and
+ * the five calls above (additions to ABI version 3; nothing above changes).
+ *
+ *   moe_add_rmsnorm   residual addition + RMS norm, bf16 and 8-bit outputs
+ *   moe_gate_logits   the router's product, bf16 x bf16 -> float32 logits
+ *   moe_route_groups  sigmoid / softmax, group-limited top-k routing
+ *   moe_quant_int8, moe_int8_matmul, moe_int8_linear
+ *                     dense projections in 8-bit integers (into and out of the
+ *                     experts' width), one scale per token and per channel
+ *
+ * The conventions above hold.  Rows: 0 <= T (M) <= 4194303.
+ * ------------------------------------------------------------------------- */
+
+/* The 8-bit output of moe_add_rmsnorm (fixed values). */
+typedef enum moe_q8 {
+  MOE_Q8_NONE = 0,
+  MOE_Q8_MXFP8 = 1,  /* E4M3 + one E8M0 per 32 elements: moe_fc1_situ's xq, xs */
+  MOE_Q8_INT8 = 2    /* int8 + one float per row: moe_int8_matmul's xq, xs */
+} moe_q8_t;
+
+/* Output type of the 8-bit integer products (fixed values). */
+typedef enum moe_out {
+  MOE_OUT_BF16 = 0,
+  MOE_OUT_F32 = 1
+} moe_out_t;
+
+/* Scores of moe_route_groups (fixed values). */
+typedef enum moe_score {
+  MOE_SCORE_SIGMOID = 0,
+  MOE_SCORE_SOFTMAX = 1
+} moe_score_t;
+
+/* What a group of experts is worth in moe_route_groups (fixed values). */
+typedef enum moe_group_score {
+  MOE_GROUP_MAX = 0,   /* its largest key */
+  MOE_GROUP_TOP2 = 1   /* the float sum of its two largest keys */
+} moe_group_score_t;
+
+/* Residual addition, root-mean-square norm and 8-bit output, in one pass.
+ *   h = x + residual in float (x alone without one), y = (h * weight) *
+ *   (1 / sqrt(mean(h^2) + eps)) in float, each output rounded once from there:
+ *   residual_out  bf16(h), or NULL for none; may be x or residual itself (the
+ *                 same pointer and stride), for an update in place.
+ *   y             bf16(y), or NULL for none (at least one of y and xq); may be
+ *                 x itself.  Other overlaps of outputs and inputs are not
+ *                 allowed.
+ *   q8            a moe_q8_t value.  MXFP8: xq uint8 [T, H], xs uint8
+ *                 [T, H/32], the rule of moe_quant_mxfp8 applied to the float
+ *                 y (H a multiple of 32).  INT8: xq int8 [T, H], xs float [T],
+ *                 the rule of moe_quant_int8 applied to the float y.  NONE: xq
+ *                 and xs are not used.
+ *   x, residual   bf16 bits [T, H], row strides ld_x, ld_residual; residual
+ *                 may be NULL.  weight: bf16 bits [H].  eps >= 0, finite.
+ *   H a multiple of 8, at most 32768; row strides >= H and multiples of 8.
+ *   A row whose squares overflow float, or that holds an infinity or a NaN,
+ *   gives what these formulas give (zeros and NaN). */
+moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ld_x, const uint16_t* residual,
+                             int64_t ld_residual, const uint16_t* weight, float eps, int T,
+                             int H, int q8, uint16_t* residual_out, int64_t ld_residual_out,
+                             uint16_t* y, int64_t ld_y, void* xq, void* xs,
+                             hipStream_t stream);
+
+/* Rows in 8-bit integers, one scale per row: s = max(absmax / 127, 2^-126),
+ * q = clamp(rint(x * (1 / s)), -127, 127), ties to even, all in float.  A row
+ * holding an infinity or a NaN gets s = NaN and q = 0, so that its products
+ * are NaN.  Tokens (one scale per token) and, at load time, weight rows (one
+ * scale per output channel) alike.
+ *   x  bf16 bits [T, H], row stride ld_x (>= H, multiple of 8); H a multiple
+ *   of 8, at most 32768.   xq  int8 [T, H] (8-byte aligned rows); xs  float [T]. */
+moe_status_t moe_quant_int8(const uint16_t* x, int64_t ld_x, int T, int H, int8_t* xq,
+                            float* xs, hipStream_t stream);
+
+/* Bytes of workspace for moe_int8_linear (and so for moe_int8_matmul) with
+ * these sizes; it grows with M.  0 for invalid sizes. */
+size_t moe_int8_workspace_size(int M, int N, int K);
+
+/* out[m, n] = (sum_k xq[m, k] * w[n, k]) * xs[m] * w_s[n]: the sum exact in
+ * int32, the three factors multiplied in float in this order, one rounding to
+ * out_type.
+ *   xq   int8 [M, K], row stride ld_xq (>= K, multiple of 16); xs float [M].
+ *   w    int8 [N, K]; w_s float [N].
+ *   out  [M, N] of out_type (a moe_out_t value), row stride ld_out >= N; 16-byte
+ *        aligned (bf16) or 4-byte aligned (float); vector stores where ld_out
+ *        is a multiple of 4 and out is 16-byte aligned.
+ *   K a multiple of 16, 16 <= K <= 131056 (no int32 overflow); 1 <= N <= 2^20.
+ *   workspace  at least moe_int8_workspace_size bytes, 256-byte aligned. */
+moe_status_t moe_int8_matmul(const int8_t* xq, int64_t ld_xq, const float* xs, const int8_t* w,
+                             const float* w_s, int M, int N, int K, int out_type, void* out,
+                             int64_t ld_out, void* workspace, size_t ws_bytes,
+                             hipStream_t stream);
+
+/* moe_quant_int8 of x [M, K] (bf16 bits, row stride ld_x), then
+ * moe_int8_matmul of the result (kept in the workspace): same output.  K at
+ * most 32768. */
+moe_status_t moe_int8_linear(const uint16_t* x, int64_t ld_x, const int8_t* w, const float* w_s,
+                             int M, int N, int K, int out_type, void* out, int64_t ld_out,
+                             void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Bytes of workspace for moe_gate_logits; can be 0 for valid sizes (then
+ * workspace may be NULL), and is 0 for invalid ones. */
+size_t moe_gate_workspace_size(int T, int E, int H);
+
+/* The router's product: logits[t, e] = sum_h x[t, h] * w[e, h], products of
+ * bf16 values summed in float (the order is fixed for given sizes).
+ *   x  bf16 bits [T, H], row stride ld_x (>= H, multiple of 8); w bf16 bits
+ *   [E, H]; logits float [T, E], row stride ld_logits >= E.
+ *   1 <= E <= 4096; H a multiple of 8, 8 <= H <= 1048576. */
+moe_status_t moe_gate_logits(const uint16_t* x, int64_t ld_x, const uint16_t* w, int T, int E,
+                             int H, float* logits, int64_t ld_logits, void* workspace,
+                             size_t ws_bytes, hipStream_t stream);
+
+/* Routing with groups of experts.
+ *   score: s_e = sigmoid(l_e), or exp(l_e - max) / sum over the unmasked
+ *   experts, evaluated in double and rounded once to float.  key_e = s_e +
+ *   bias_e in float (bias NULL: s_e).  An expert is masked for a token when its
+ *   logit is -inf or the lowest finite float, or its key is -inf.
+ *   The experts stand in n_group groups of E / n_group neighbours; the
+ *   topk_group groups of most worth (group_score; masked experts do not count)
+ *   stay, and of their experts the top_k with the largest keys, in descending
+ *   order.  Equal worths and equal keys rank the lower index first; NaN ranks
+ *   below every number.  A group of masked experts only ranks last.
+ *   w_k = s_k, divided by sum_j s_j (double, left to right; 0 where that sum
+ *   is 0) if renormalise is not 0, times routed_scaling, rounded to float.
+ *   Slots for which no unmasked expert is left hold id -1 and weight 0 (the
+ *   masked slots of moe_permute); a token whose experts are all masked gets
+ *   only those.
+ *   topk_idx int32 [T, top_k], topk_w float [T, top_k].
+ *   With one group, sigmoid, renormalise and no masked expert the results are
+ *   those of moe_route.
+ *   1 <= top_k <= min(64, topk_group * (E / n_group)); 1 <= topk_group <=
+ *   n_group <= 64; E a multiple of n_group, at most 4096. */
+moe_status_t moe_route_groups(const float* logits, int64_t ld_logits, const float* bias, int T,
+                              int E, int top_k, int n_group, int topk_group, int score,
+                              int group_score, int renormalise, float routed_scaling,
+                              int32_t* topk_idx, float* topk_w, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,12 +10,25 @@ from ._binding import (  # noqa: F401
     COMBINE_ATOMIC,
     COMBINE_DETERMINISTIC,
     EXPORTS,
+    GROUP_MAX,
+    GROUP_TOP2,
     MoEError,
+    Q8_INT8,
+    Q8_MXFP8,
+    Q8_NONE,
+    SCORE_SIGMOID,
+    SCORE_SOFTMAX,
     lib,
     load_library,
     moe_abi_version,
+    moe_add_rmsnorm,
     moe_fc1_situ,
     moe_fc2_combine,
+    moe_gate_logits,
+    moe_gate_workspace_size,
+    moe_int8_linear,
+    moe_int8_matmul,
+    moe_int8_workspace_size,
     moe_permute,
     moe_permute_noalloc,
     W13_GATE_UP,
@@ -24,9 +37,11 @@ from ._binding import (  # noqa: F401
     moe_prepack_w13,
     moe_prepack_w13_layout,
     moe_prepack_w2,
+    moe_quant_int8,
     moe_quant_mxfp8,
     moe_quant_permute,
     moe_route,
+    moe_route_groups,
     moe_route_quant_permute,
     moe_workspace_size,
 )

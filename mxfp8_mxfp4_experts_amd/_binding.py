@@ -29,12 +29,21 @@ EXPORTS = (
     "moe_permute", "moe_fc1_situ", "moe_fc2_combine", "moe_prepack_w13", "moe_prepack_w2",
     "moe_fc1_situ_tiled", "moe_fc2_combine_tiled", "moe_route_quant_permute",
     "moe_prepack_w13_layout", "moe_permute_noalloc", "moe_quant_permute",
+    "moe_add_rmsnorm", "moe_quant_int8", "moe_int8_workspace_size", "moe_int8_matmul",
+    "moe_int8_linear", "moe_gate_workspace_size", "moe_gate_logits", "moe_route_groups",
 )
 
 # moe_w13_layout_t values (row order of a w13 tensor)
 W13_GATE_UP, W13_UP_GATE, W13_INTERLEAVED = 0, 1, 2
 # moe_combine_t values (how moe_fc2_combine sums a token's top-k rows)
 COMBINE_DETERMINISTIC, COMBINE_ATOMIC = 0, 1
+# moe_q8_t values (the 8-bit output of moe_add_rmsnorm)
+Q8_NONE, Q8_MXFP8, Q8_INT8 = 0, 1, 2
+# moe_out_t values, by output dtype
+_OUT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+# moe_score_t and moe_group_score_t values (moe_route_groups)
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -84,6 +93,22 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
         getattr(lib, name).argtypes = [_P, _P, _I, _I, _I, _P, _P, _P]
     lib.moe_prepack_w13_layout.restype = _I
     lib.moe_prepack_w13_layout.argtypes = [_P, _P, _I, _I, _I, _I, _P, _P, _P]
+    lib.moe_add_rmsnorm.restype = _I
+    lib.moe_add_rmsnorm.argtypes = [_P, _I64, _P, _I64, _P, _F, _I, _I, _I, _P, _I64, _P, _I64,
+                                    _P, _P, _P]
+    lib.moe_quant_int8.restype = _I
+    lib.moe_quant_int8.argtypes = [_P, _I64, _I, _I, _P, _P, _P]
+    for name in ("moe_int8_workspace_size", "moe_gate_workspace_size"):
+        getattr(lib, name).restype = _SZ
+        getattr(lib, name).argtypes = [_I, _I, _I]
+    lib.moe_int8_matmul.restype = _I
+    lib.moe_int8_matmul.argtypes = [_P, _I64, _P, _P, _P, _I, _I, _I, _I, _P, _I64, _P, _SZ, _P]
+    lib.moe_int8_linear.restype = _I
+    lib.moe_int8_linear.argtypes = [_P, _I64, _P, _P, _I, _I, _I, _I, _P, _I64, _P, _SZ, _P]
+    lib.moe_gate_logits.restype = _I
+    lib.moe_gate_logits.argtypes = [_P, _I64, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]
+    lib.moe_route_groups.restype = _I
+    lib.moe_route_groups.argtypes = [_P, _I64, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P]
     return lib
 
 
@@ -437,3 +462,230 @@ def moe_prepack_w2(w2, w2_s):
     shapes)."""
     E, H, I = _weight_pair("moe_prepack_w2", w2, w2_s)
     return _prepack("moe_prepack_w2", w2, w2_s, H, I)
+
+
+# ---------------------------------------------------------------------------
+# Around the experts.  These run a few microseconds each in a decode step, so
+# their checks are kept short: one comparison per property.
+
+_BF16, _F32, _U8, _I8, _I32 = (torch.bfloat16, torch.float32, torch.uint8, torch.int8,
+                               torch.int32)
+
+
+def _rows(t, name, dtype, shape, device):
+    """A [T, C] tensor whose rows may be strided; returns its row stride."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    ld, one = t.stride()
+    if one != 1 and shape[1] != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return ld if shape[0] > 1 else shape[1]   # the stride of a single row says nothing
+
+
+def _dense(t, name, dtype, shape, device):
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _begin(x, name):
+    """The device and its current stream for a call whose main operand is x."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    dev = x.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev}, which is not the current device")
+    return dev, torch.cuda.current_stream().cuda_stream
+
+
+def _workspace(ws, need, dev, name):
+    if ws is None:
+        return torch.empty(need, dtype=_U8, device=dev)
+    if ws.dtype is not _U8 or ws.device != dev or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on " + str(dev))
+    if ws.numel() < need:
+        raise ValueError(f"{name} needs {need} bytes of workspace, got {ws.numel()}")
+    return ws
+
+
+def moe_add_rmsnorm(x, weight, eps: float, residual=None, q8: int = Q8_NONE, residual_out=None,
+                    y=None, want_y: bool = True, xq=None, xs=None):
+    """h = x + residual, y = h * weight / sqrt(mean(h^2) + eps), and y in 8
+    bits.  Returns ``(residual_out, y, xq, xs)``: bf16(h) (None without a
+    residual, unless a buffer is given), bf16(y) (None with ``want_y=False``
+    and no buffer), and for ``q8`` Q8_MXFP8 uint8 [T, H] and [T, H/32], for
+    Q8_INT8 int8 [T, H] and float [T], else None.  ``residual_out`` may be
+    ``x`` or ``residual`` itself."""
+    dev, stream = _begin(x, "x")
+    shape = x.shape
+    T, H = shape
+    ld_x = _rows(x, "x", _BF16, shape, dev)
+    _dense(weight, "weight", _BF16, (H,), dev)
+    ld_r = ld_h = ld_y = 0
+    if residual is not None:
+        ld_r = _rows(residual, "residual", _BF16, shape, dev)
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=_BF16, device=dev)
+    if residual_out is not None:
+        ld_h = _rows(residual_out, "residual_out", _BF16, shape, dev)
+    if y is None and want_y:
+        y = torch.empty(shape, dtype=_BF16, device=dev)
+    if y is not None:
+        ld_y = _rows(y, "y", _BF16, shape, dev)
+    if q8 == Q8_MXFP8 or q8 == Q8_INT8:
+        kind, s_shape, s_kind = (_U8, (T, H // 32), _U8) if q8 == Q8_MXFP8 else (_I8, (T,), _F32)
+        if xq is None:
+            xq = torch.empty(shape, dtype=kind, device=dev)
+        if xs is None:
+            xs = torch.empty(s_shape, dtype=s_kind, device=dev)
+        _dense(xq, "xq", kind, shape, dev)
+        _dense(xs, "xs", s_kind, s_shape, dev)
+    else:
+        xq = xs = None
+    st = lib().moe_add_rmsnorm(x.data_ptr(), ld_x, _ptr(residual), ld_r, weight.data_ptr(), eps, T,
+                               H, q8, _ptr(residual_out), ld_h, _ptr(y), ld_y, _ptr(xq), _ptr(xs),
+                               stream)
+    if st:
+        raise MoEError("moe_add_rmsnorm", st)
+    return residual_out, y, xq, xs
+
+
+def moe_quant_int8(x, xq=None, xs=None):
+    """bf16 rows [T, H] -> int8 [T, H] and one float scale per row [T]."""
+    dev, stream = _begin(x, "x")
+    ld_x = _rows(x, "x", _BF16, x.shape, dev)
+    T, H = x.shape
+    if xq is None:
+        xq = torch.empty((T, H), dtype=_I8, device=dev)
+    if xs is None:
+        xs = torch.empty((T,), dtype=_F32, device=dev)
+    _dense(xq, "xq", _I8, (T, H), dev)
+    _dense(xs, "xs", _F32, (T,), dev)
+    st = lib().moe_quant_int8(x.data_ptr(), ld_x, T, H, xq.data_ptr(), xs.data_ptr(), stream)
+    if st:
+        raise MoEError("moe_quant_int8", st)
+    return xq, xs
+
+
+def moe_int8_workspace_size(M: int, N: int, K: int) -> int:
+    """Workspace bytes of moe_int8_linear and moe_int8_matmul."""
+    n = lib().moe_int8_workspace_size(M, N, K)
+    if n == 0:
+        raise ValueError("invalid sizes for moe_int8_workspace_size")
+    return n
+
+
+def _int8_out(out, out_dtype, M, N, dev):
+    if out is None:
+        if out_dtype not in _OUT_TYPE:
+            raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    elif out.dtype not in _OUT_TYPE:
+        raise ValueError(f"out must be bfloat16 or float32, got {out.dtype}")
+    return out, _rows(out, "out", out.dtype, (M, N), dev), _OUT_TYPE[out.dtype]
+
+
+def _int8_weight(w, w_s, K, dev):
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[1] != K:
+        raise ValueError(f"w must be [N, {K}]")
+    N = w.shape[0]
+    _dense(w, "w", _I8, (N, K), dev)
+    _dense(w_s, "w_s", _F32, (N,), dev)
+    return N
+
+
+def moe_int8_matmul(xq, xs, w, w_s, out=None, out_dtype=torch.bfloat16, workspace=None):
+    """out [M, N] = (xq [M, K] . w [N, K]) * xs [M] * w_s [N], the sum exact in
+    int32; ``out`` or ``out_dtype`` says bf16 or float32."""
+    dev, stream = _begin(xq, "xq")
+    M, K = xq.shape
+    ld_xq = _rows(xq, "xq", _I8, xq.shape, dev)
+    _dense(xs, "xs", _F32, (M,), dev)
+    N = _int8_weight(w, w_s, K, dev)
+    out, ld_out, kind = _int8_out(out, out_dtype, M, N, dev)
+    L = lib()
+    workspace = _workspace(workspace, L.moe_int8_workspace_size(M, N, K) if workspace is None
+                           else 0, dev, "moe_int8_matmul")
+    st = L.moe_int8_matmul(xq.data_ptr(), ld_xq, xs.data_ptr(), w.data_ptr(), w_s.data_ptr(), M, N,
+                           K, kind, out.data_ptr(), ld_out, workspace.data_ptr(),
+                           workspace.numel(), stream)
+    if st:
+        raise MoEError("moe_int8_matmul", st)
+    return out
+
+
+def moe_int8_linear(x, w, w_s, out=None, out_dtype=torch.bfloat16, workspace=None):
+    """moe_quant_int8 of x [M, K] (bf16) and moe_int8_matmul as one call."""
+    dev, stream = _begin(x, "x")
+    M, K = x.shape
+    ld_x = _rows(x, "x", _BF16, x.shape, dev)
+    N = _int8_weight(w, w_s, K, dev)
+    out, ld_out, kind = _int8_out(out, out_dtype, M, N, dev)
+    L = lib()
+    workspace = _workspace(workspace, L.moe_int8_workspace_size(M, N, K) if workspace is None
+                           else 0, dev, "moe_int8_linear")
+    st = L.moe_int8_linear(x.data_ptr(), ld_x, w.data_ptr(), w_s.data_ptr(), M, N, K, kind,
+                           out.data_ptr(), ld_out, workspace.data_ptr(), workspace.numel(), stream)
+    if st:
+        raise MoEError("moe_int8_linear", st)
+    return out
+
+
+def moe_gate_workspace_size(T: int, E: int, H: int) -> int:
+    """Workspace bytes of moe_gate_logits (0 where it needs none)."""
+    return lib().moe_gate_workspace_size(T, E, H)
+
+
+def moe_gate_logits(x, w, out=None, workspace=None):
+    """Router logits float [T, E] of x [T, H] and w [E, H], both bf16."""
+    dev, stream = _begin(x, "x")
+    T, H = x.shape
+    ld_x = _rows(x, "x", _BF16, x.shape, dev)
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError(f"w must be [E, {H}]")
+    E = w.shape[0]
+    _dense(w, "w", _BF16, (E, H), dev)
+    if out is None:
+        out = torch.empty((T, E), dtype=_F32, device=dev)
+    ld_out = _rows(out, "out", _F32, (T, E), dev)
+    L = lib()
+    workspace = _workspace(workspace, L.moe_gate_workspace_size(T, E, H) if workspace is None
+                           else 0, dev, "moe_gate_logits")
+    st = L.moe_gate_logits(x.data_ptr(), ld_x, w.data_ptr(), T, E, H, out.data_ptr(), ld_out,
+                           workspace.data_ptr(), workspace.numel(), stream)
+    if st:
+        raise MoEError("moe_gate_logits", st)
+    return out
+
+
+def moe_route_groups(logits, bias, top_k: int, n_group: int = 1, topk_group: int = 1,
+                     score: int = SCORE_SIGMOID, group_score: int = GROUP_TOP2,
+                     renormalise: bool = True, routed_scaling: float = 1.0, topk_idx=None,
+                     topk_w=None):
+    """Group-limited top-k routing of float logits [T, E]: ids int32 and
+    weights float [T, top_k]; -1 with weight 0 where no unmasked expert is
+    left.  ``score``: SCORE_SIGMOID or SCORE_SOFTMAX; ``group_score``:
+    GROUP_MAX or GROUP_TOP2."""
+    dev, stream = _begin(logits, "logits")
+    T, E = logits.shape
+    ld = _rows(logits, "logits", _F32, logits.shape, dev)
+    if bias is not None:
+        _dense(bias, "bias", _F32, (E,), dev)
+    shape = (T, top_k)
+    if topk_idx is None:
+        topk_idx = torch.empty(shape, dtype=_I32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty(shape, dtype=_F32, device=dev)
+    _dense(topk_idx, "topk_idx", _I32, shape, dev)
+    _dense(topk_w, "topk_w", _F32, shape, dev)
+    st = lib().moe_route_groups(logits.data_ptr(), ld, _ptr(bias), T, E, top_k, n_group,
+                                topk_group, score, group_score, 1 if renormalise else 0,
+                                routed_scaling, topk_idx.data_ptr(), topk_w.data_ptr(), stream)
+    if st:
+        raise MoEError("moe_route_groups", st)
+    return topk_idx, topk_w

@@ -56,6 +56,45 @@ bool valid_rows(int T, int top_k, int H, int I) {
   return R * wide < ((int64_t)1 << 46);
 }
 
+// The calls around the experts.
+bool valid_norm_rows(int T, int H) {
+  return T >= 0 && T <= kMaxRows && H >= 8 && H <= kMaxNormH && H % 8 == 0;
+}
+bool valid_int8(int M, int N, int K) {
+  return M >= 0 && M <= kMaxRows && N >= 1 && N <= kMaxInt8N && K >= 16 && K <= kMaxInt8K &&
+         K % 16 == 0;
+}
+bool valid_gate(int T, int E, int H) {
+  return T >= 0 && T <= kMaxRows && E >= 1 && E <= kMaxExperts && H >= 8 && H <= kMaxGateH &&
+         H % 8 == 0;
+}
+
+// Workspace of moe_int8_linear: partial sums of the product at its start,
+// then the tokens in 8 bits and their scales.
+struct Int8Layout {
+  size_t xq, xs, total;
+};
+Int8Layout int8_layout(int M, int N, int K) {
+  Int8Layout l;
+  l.xq = align256(dense_workspace(true, M, N, K));
+  l.xs = align256(l.xq + (size_t)M * K);
+  l.total = align256(l.xs + sizeof(float) * (size_t)M + 1);
+  return l;
+}
+
+NormParams quant_params(const uint16_t* x, int64_t ld_x, int T, int H, int8_t* xq, float* xs) {
+  return NormParams{x, ld_x, nullptr, 0, nullptr, 0.0f, T, H, nullptr, 0, nullptr, 0,
+                    reinterpret_cast<uint8_t*>(xq), reinterpret_cast<uint8_t*>(xs)};
+}
+
+DenseParams int8_params(const int8_t* xq, int64_t ld_xq, const float* xs, const int8_t* w,
+                        const float* w_s, int M, int N, int K, int out_type, void* out,
+                        int64_t ld_out, void* workspace) {
+  return DenseParams{reinterpret_cast<const uint8_t*>(xq), ld_xq,
+                     reinterpret_cast<const uint8_t*>(w), K, M, N, K, xs, w_s, out, ld_out,
+                     out_type == MOE_OUT_F32, ld_out % 4 == 0 && aligned(out, 16), workspace};
+}
+
 }  // namespace
 
 extern "C" {
@@ -362,6 +401,142 @@ moe_status_t moe_prepack_w13_layout(const uint8_t* w13, const uint8_t* w13_s, in
 moe_status_t moe_prepack_w2(const uint8_t* w2, const uint8_t* w2_s, int E_local, int H, int I,
                             uint8_t* w2t, uint8_t* w2t_s, hipStream_t stream) {
   return prepack_impl(false, w2, w2_s, E_local, H, I, MOE_W13_GATE_UP, w2t, w2t_s, stream);
+}
+
+moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ld_x, const uint16_t* residual,
+                             int64_t ld_residual, const uint16_t* weight, float eps, int T,
+                             int H, int q8, uint16_t* residual_out, int64_t ld_residual_out,
+                             uint16_t* y, int64_t ld_y, void* xq, void* xs,
+                             hipStream_t stream) {
+  if (q8 < MOE_Q8_NONE || q8 > MOE_Q8_INT8) return MOE_ERR_ENUM;
+  if (!valid_norm_rows(T, H) || ld_x < H || (residual && ld_residual < H) ||
+      (residual_out && ld_residual_out < H) || (y && ld_y < H) ||
+      (q8 == MOE_Q8_MXFP8 && H % 32 != 0))
+    return MOE_ERR_SHAPE;
+  if (!(eps >= 0.0f) || !(eps <= 3.402823466e38f)) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!x || !weight || (!y && q8 == MOE_Q8_NONE) || (q8 != MOE_Q8_NONE && (!xq || !xs)))
+    return MOE_ERR_NULL;
+  if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(weight, 16) ||
+      (residual && (!aligned(residual, 16) || ld_residual % 8 != 0)) ||
+      (residual_out && (!aligned(residual_out, 16) || ld_residual_out % 8 != 0)) ||
+      (y && (!aligned(y, 16) || ld_y % 8 != 0)) ||
+      (q8 != MOE_Q8_NONE && (!aligned(xq, 16) || !aligned(xs, 4))))
+    return MOE_ERR_ALIGN;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  const NormParams p{x, ld_x, residual, ld_residual, weight, eps, T, H, residual_out,
+                     ld_residual_out, y, ld_y, static_cast<uint8_t*>(xq),
+                     static_cast<uint8_t*>(xs)};
+  return finish(launch_norm(p, q8, true, stream));
+}
+
+moe_status_t moe_quant_int8(const uint16_t* x, int64_t ld_x, int T, int H, int8_t* xq,
+                            float* xs, hipStream_t stream) {
+  if (!valid_norm_rows(T, H) || ld_x < H) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!x || !xq || !xs) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(xq, 16) || !aligned(xs, 4))
+    return MOE_ERR_ALIGN;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  return finish(launch_norm(quant_params(x, ld_x, T, H, xq, xs), MOE_Q8_INT8, false, stream));
+}
+
+size_t moe_int8_workspace_size(int M, int N, int K) {
+  if (!valid_int8(M, N, K)) return 0;
+  return int8_layout(M, N, K).total;
+}
+
+moe_status_t moe_int8_matmul(const int8_t* xq, int64_t ld_xq, const float* xs, const int8_t* w,
+                             const float* w_s, int M, int N, int K, int out_type, void* out,
+                             int64_t ld_out, void* workspace, size_t ws_bytes,
+                             hipStream_t stream) {
+  if (out_type != MOE_OUT_BF16 && out_type != MOE_OUT_F32) return MOE_ERR_ENUM;
+  if (!valid_int8(M, N, K) || ld_xq < K || ld_out < N) return MOE_ERR_SHAPE;
+  if (M == 0) return MOE_OK;
+  const Int8Layout l = int8_layout(M, N, K);
+  if (!xq || !xs || !w || !w_s || !out || (!workspace && l.xq > 0)) return MOE_ERR_NULL;
+  if (!aligned(xq, 16) || ld_xq % 16 != 0 || !aligned(w, 16) || !aligned(xs, 4) ||
+      !aligned(w_s, 4) || !aligned(out, out_type == MOE_OUT_F32 ? 4 : 16) ||
+      !aligned(workspace, 256))
+    return MOE_ERR_ALIGN;
+  if (ws_bytes < l.xq) return MOE_ERR_WORKSPACE;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  return finish(launch_dense(
+      true, int8_params(xq, ld_xq, xs, w, w_s, M, N, K, out_type, out, ld_out, workspace),
+      stream));
+}
+
+moe_status_t moe_int8_linear(const uint16_t* x, int64_t ld_x, const int8_t* w, const float* w_s,
+                             int M, int N, int K, int out_type, void* out, int64_t ld_out,
+                             void* workspace, size_t ws_bytes, hipStream_t stream) {
+  if (out_type != MOE_OUT_BF16 && out_type != MOE_OUT_F32) return MOE_ERR_ENUM;
+  if (!valid_int8(M, N, K) || K > kMaxNormH || ld_x < K || ld_out < N) return MOE_ERR_SHAPE;
+  if (M == 0) return MOE_OK;
+  if (!x || !w || !w_s || !out || !workspace) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(w, 16) || !aligned(w_s, 4) ||
+      !aligned(out, out_type == MOE_OUT_F32 ? 4 : 16) || !aligned(workspace, 256))
+    return MOE_ERR_ALIGN;
+  const Int8Layout l = int8_layout(M, N, K);
+  if (ws_bytes < l.total) return MOE_ERR_WORKSPACE;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  int8_t* xq = reinterpret_cast<int8_t*>(static_cast<char*>(workspace) + l.xq);
+  float* xs = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.xs);
+  if (launch_norm(quant_params(x, ld_x, M, K, xq, xs), MOE_Q8_INT8, false, stream) != hipSuccess)
+    return MOE_ERR_HIP;
+  return finish(launch_dense(
+      true, int8_params(xq, K, xs, w, w_s, M, N, K, out_type, out, ld_out, workspace), stream));
+}
+
+size_t moe_gate_workspace_size(int T, int E, int H) {
+  if (!valid_gate(T, E, H)) return 0;
+  return dense_workspace(false, T, E, 2 * (int64_t)H);
+}
+
+moe_status_t moe_gate_logits(const uint16_t* x, int64_t ld_x, const uint16_t* w, int T, int E,
+                             int H, float* logits, int64_t ld_logits, void* workspace,
+                             size_t ws_bytes, hipStream_t stream) {
+  if (!valid_gate(T, E, H) || ld_x < H || ld_logits < E) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  const size_t need = dense_workspace(false, T, E, 2 * (int64_t)H);
+  if (!x || !w || !logits || (!workspace && need > 0)) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(w, 16) || !aligned(logits, 4) ||
+      !aligned(workspace, 256))
+    return MOE_ERR_ALIGN;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  const DenseParams p{reinterpret_cast<const uint8_t*>(x), 2 * ld_x,
+                      reinterpret_cast<const uint8_t*>(w), 2 * (int64_t)H, T, E, 2 * H, nullptr,
+                      nullptr, logits, ld_logits, 1,
+                      ld_logits % 4 == 0 && aligned(logits, 16), workspace};
+  return finish(launch_dense(false, p, stream));
+}
+
+moe_status_t moe_route_groups(const float* logits, int64_t ld_logits, const float* bias, int T,
+                              int E, int top_k, int n_group, int topk_group, int score,
+                              int group_score, int renormalise, float routed_scaling,
+                              int32_t* topk_idx, float* topk_w, hipStream_t stream) {
+  if (T < 0 || T > kMaxRows || E < 1 || E > kMaxExperts || n_group < 1 || n_group > kMaxGroups ||
+      E % n_group != 0 || topk_group < 1 || topk_group > n_group || top_k < 1 ||
+      top_k > kMaxTopK || top_k > topk_group * (E / n_group) || ld_logits < E)
+    return MOE_ERR_SHAPE;
+  if ((score != MOE_SCORE_SIGMOID && score != MOE_SCORE_SOFTMAX) ||
+      (group_score != MOE_GROUP_MAX && group_score != MOE_GROUP_TOP2))
+    return MOE_ERR_ENUM;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !topk_w) return MOE_ERR_NULL;
+  if (!aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) ||
+      (bias && !aligned(bias, 4)))
+    return MOE_ERR_ALIGN;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  const RouteGroupsParams p{logits, ld_logits, bias, T, E, top_k, n_group, topk_group, score,
+                            group_score, renormalise != 0, routed_scaling, topk_idx, topk_w};
+  return finish(launch_route_groups(p, stream));
 }
 
 }  // extern "C"

@@ -11,6 +11,12 @@ namespace mi355moe {
 // Limits checked at the C ABI.
 constexpr int kMaxExperts = 4096;   // routing width E and local window E_local
 constexpr int kMaxTopK = 64;        // one wavefront lane per selected slot
+constexpr int kMaxGroups = 64;      // expert groups of moe_route_groups
+constexpr int kMaxRows = (1 << 22) - 1;   // rows of the calls around the experts
+constexpr int kMaxNormH = 32768;    // row width of the norm (1024 threads, 32 elements each)
+constexpr int kMaxInt8K = 131056;   // 128 * 128 * K < 2^31
+constexpr int kMaxInt8N = 1 << 20;
+constexpr int kMaxGateH = 1 << 20;
 constexpr int kGroup = 32;          // MX block: one E8M0 scale per 32 elements
 
 // FC tile heights (token rows per workgroup tile) for which moe_permute

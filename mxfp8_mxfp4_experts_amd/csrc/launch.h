@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/mi355moe.h"
+
 namespace mi355moe {
 
 hipError_t launch_route(const float* logits, int64_t ld, const float* bias, int T, int E, int K,
@@ -67,5 +69,55 @@ hipError_t launch_combine(const uint16_t* y, const int8_t* ye, int H, const int3
 hipError_t launch_acc_clear(float* acc, int T, int H, hipStream_t stream);
 hipError_t launch_acc_to_bf16(const float* acc, int T, int H, uint16_t* out, int64_t ld_out,
                               hipStream_t stream);
+
+// Around the experts.
+// Residual addition + RMS norm + 8-bit output (norm.hip); norm false: the
+// INT8 quantisation of x alone.
+struct NormParams {
+  const uint16_t* x;
+  int64_t ld_x;
+  const uint16_t* res;      // may be null
+  int64_t ld_res;
+  const uint16_t* weight;
+  float eps;
+  int T, H;
+  uint16_t* h;              // may be null
+  int64_t ld_h;
+  uint16_t* y;              // may be null
+  int64_t ld_y;
+  uint8_t* xq;
+  uint8_t* xs;              // E8M0 bytes (MXFP8) or floats (INT8)
+};
+hipError_t launch_norm(const NormParams& p, int q8, bool norm, hipStream_t stream);
+
+// Group-limited routing (route_groups.hip).
+struct RouteGroupsParams {
+  const float* logits;
+  int64_t ld;
+  const float* bias;        // may be null
+  int T, E, K, n_group, topk_group, score, group_score, renormalise;
+  float scaling;
+  int32_t* topk_idx;
+  float* topk_w;
+};
+hipError_t launch_route_groups(const RouteGroupsParams& p, hipStream_t stream);
+
+// Dense products (dense.hip): operands as bytes along K.
+struct DenseParams {
+  const uint8_t* a;         // [M, Kb], row stride ld_a bytes
+  int64_t ld_a;
+  const uint8_t* b;         // [N, Kb], row stride ld_b bytes
+  int64_t ld_b;
+  int M, N, Kb;
+  const float* sx;          // INT8: [M], [N] scales
+  const float* sw;
+  void* out;
+  int64_t ld_out;           // elements
+  int out_f32;
+  int out_vec;              // rows take 4-element vector stores
+  void* partial;            // dense_workspace bytes
+};
+size_t dense_workspace(bool i8, int M, int N, int64_t Kb);
+hipError_t launch_dense(bool i8, const DenseParams& p, hipStream_t stream);
 
 }  // namespace mi355moe

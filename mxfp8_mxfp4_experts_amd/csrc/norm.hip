@@ -1,0 +1,224 @@
+// Residual addition + root-mean-square norm + 8-bit output, and the 8-bit
+// integer quantisation of plain rows.
+//
+//   h = x + r (float32; stored as bf16),   rstd = 1 / sqrt(mean(h^2) + eps),
+//   y = (h * w) * rstd (float32; stored as bf16 if wanted), and y in 8 bits:
+//   MXFP8 with the rule of moe_quant_mxfp8, or INT8 with one float scale per
+//   row, s = max(absmax / 127, 2^-126), q = rint(y * (1 / s)).
+//
+// The norm and the 8-bit rounding start from the float32 sum, not from its
+// bf16 copy: y is rounded once on its way to each output.
+//
+// One workgroup per row, one pass: the row stays in registers between the
+// reduction and the outputs.  Rounding is monotone, so the largest |y| is the
+// largest |h * w| times rstd exactly, and the sum of squares and the absolute
+// maximum are reduced together with one barrier.
+#include "common.h"
+#include "fc_common.h"   // e4m3x4_scaled
+#include "launch.h"
+
+namespace mi355moe {
+
+namespace {
+
+constexpr float kMinScale = 1.17549435e-38f;   // 2^-126: 1 / s stays finite
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+// NaN counts as the largest value: a row that holds one must not hide it.
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)v, off);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+    f[2 * i + 1] = bf16_to_f32(w[i] >> 16);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16(f[2 * i]) | (f32_to_bf16(f[2 * i + 1]) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Whole numbers of [-127, 127] of 8 values; inv = 1 / s.
+__device__ __forceinline__ uint2 int8x8(const float (&f)[8], float inv) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float r = fminf(fmaxf(__builtin_rintf(f[i] * inv), -127.0f), 127.0f);
+    w[i >> 2] |= ((uint32_t)(int)r & 0xFFu) << (8 * (i & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// MXFP8 codes of a lane's 8 values and its 32-element group's scale byte;
+// the group is four consecutive lanes.
+__device__ __forceinline__ uint2 mxfp8x8(const float (&f)[8], uint32_t& scale) {
+  float amax = 0.0f;
+  uint32_t odd = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = fabsf(f[i]);
+    amax = a > amax ? a : amax;   // NaN compares false: ignored
+    odd |= (__float_as_uint(f[i]) & 0x7F800000u) == 0x7F800000u;
+  }
+  amax = fmaxf(amax, __shfl_xor(amax, 1));
+  amax = fmaxf(amax, __shfl_xor(amax, 2));
+  odd |= __shfl_xor(odd, 1);
+  odd |= __shfl_xor(odd, 2);
+  const int e = mx8_exponent(amax);
+  scale = (uint32_t)(e + 127);
+  uint32_t lo = 0, hi = 0;
+  if (!odd && e > -127) {
+    const float s2 = __uint_as_float((uint32_t)(e + 127) << 23);
+    lo = e4m3x4_scaled(f[0], f[1], f[2], f[3], s2);
+    hi = e4m3x4_scaled(f[4], f[5], f[6], f[7], s2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lo |= e4m3_encode(ldexpf(f[i], -e)) << (8 * i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) hi |= e4m3_encode(ldexpf(f[4 + i], -e)) << (8 * i);
+  }
+  return make_uint2(lo, hi);
+}
+
+// One row per workgroup, P 8-element pieces per thread (piece tid + i *
+// blockDim).  NORM false: y = x (the 8-bit quantisation alone).
+template <int P, int Q8, bool NORM>
+__global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
+  __shared__ float sum_s[16];
+  __shared__ uint32_t max_s[16];
+  const int tid = threadIdx.x, n = p.H / 8;
+  const int64_t row = blockIdx.x;
+  const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.ld_x);
+  const uint4* r = reinterpret_cast<const uint4*>(p.res + (p.res ? row * p.ld_res : 0));
+  const uint4* w = reinterpret_cast<const uint4*>(p.weight);
+
+  uint4 xv[P], rv[P], wv[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int c = tid + i * (int)blockDim.x;
+    if (c < n) {
+      xv[i] = x[c];
+      if (NORM && p.res) rv[i] = r[c];
+      if (NORM) wv[i] = w[c];
+    }
+  }
+  float f[P][8];
+  float sum = 0.0f;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int c = tid + i * (int)blockDim.x;
+    if (c >= n) continue;
+    unpack8(xv[i], f[i]);
+    if constexpr (NORM) {
+      if (p.res) {
+        float g[8];
+        unpack8(rv[i], g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] += g[j];
+      }
+      if (p.h) reinterpret_cast<uint4*>(p.h + row * p.ld_h)[c] = pack8(f[i]);
+      float g[8];
+      unpack8(wv[i], g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sum += f[i][j] * f[i][j];
+        f[i][j] *= g[j];
+      }
+    }
+    if constexpr (Q8 == MOE_Q8_INT8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t a = __float_as_uint(f[i][j]) & 0x7FFFFFFFu;
+        top = a > top ? a : top;
+      }
+    }
+  }
+  // Every wavefront adds the wavefronts' sums in the same order.
+  const int wave = tid >> 6, n_waves = (int)blockDim.x >> 6;
+  if constexpr (NORM) sum = wave_sum(sum);
+  if constexpr (Q8 == MOE_Q8_INT8) top = wave_umax(top);
+  if ((tid & 63) == 0) {
+    if constexpr (NORM) sum_s[wave] = sum;
+    if constexpr (Q8 == MOE_Q8_INT8) max_s[wave] = top;
+  }
+  __syncthreads();
+  sum = 0.0f;
+  top = 0;
+  for (int i = 0; i < n_waves; ++i) {
+    if constexpr (NORM) sum += sum_s[i];
+    if constexpr (Q8 == MOE_Q8_INT8) top = max_s[i] > top ? max_s[i] : top;
+  }
+  const float rstd = NORM ? 1.0f / sqrtf(sum / (float)p.H + p.eps) : 1.0f;
+  float inv = 0.0f;
+  bool odd = false;
+  if constexpr (Q8 == MOE_Q8_INT8) {
+    const float amax = NORM ? __uint_as_float(top) * rstd : __uint_as_float(top);
+    odd = !(amax <= 3.402823466e38f);   // the row holds an infinity or a NaN
+    const float s = fmaxf(amax / 127.0f, kMinScale);
+    inv = 1.0f / s;
+    if (tid == 0) reinterpret_cast<float*>(p.xs)[row] = odd ? __uint_as_float(0x7FC00000u) : s;
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int c = tid + i * (int)blockDim.x;
+    const bool in = c < n;   // alike for the four lanes of a 32-element group
+    if (!in) continue;
+    if constexpr (NORM) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[i][j] *= rstd;
+      if (p.y) reinterpret_cast<uint4*>(p.y + row * p.ld_y)[c] = pack8(f[i]);
+    }
+    if constexpr (Q8 == MOE_Q8_INT8) {
+      reinterpret_cast<uint2*>(p.xq + row * p.H)[c] = odd ? make_uint2(0, 0) : int8x8(f[i], inv);
+    }
+    if constexpr (Q8 == MOE_Q8_MXFP8) {
+      uint32_t scale;
+      const uint2 q = mxfp8x8(f[i], scale);
+      reinterpret_cast<uint2*>(p.xq + row * p.H)[c] = q;
+      if ((c & 3) == 0) p.xs[row * (p.H / 32) + c / 4] = (uint8_t)scale;
+    }
+  }
+}
+
+template <int P>
+hipError_t launch_p(const NormParams& p, int q8, bool norm, int threads, hipStream_t stream) {
+  const dim3 grid(p.T), block(threads);
+  if (!norm)
+    hipLaunchKernelGGL((norm_kernel<P, MOE_Q8_INT8, false>), grid, block, 0, stream, p);
+  else if (q8 == MOE_Q8_NONE)
+    hipLaunchKernelGGL((norm_kernel<P, MOE_Q8_NONE, true>), grid, block, 0, stream, p);
+  else if (q8 == MOE_Q8_MXFP8)
+    hipLaunchKernelGGL((norm_kernel<P, MOE_Q8_MXFP8, true>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((norm_kernel<P, MOE_Q8_INT8, true>), grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormParams& p, int q8, bool norm, hipStream_t stream) {
+  const int pieces = p.H / 8;
+  const int per = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : 4;   // H <= kMaxNormH = 32768
+  const int threads = ((pieces + per - 1) / per + 63) / 64 * 64;
+  if (per == 1) return launch_p<1>(p, q8, norm, threads, stream);
+  if (per == 2) return launch_p<2>(p, q8, norm, threads, stream);
+  return launch_p<4>(p, q8, norm, threads, stream);
+}
+
+}  // namespace mi355moe
