@@ -141,4 +141,12 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float v) {
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
 
+// Two floats -> two bf16 in one dword (a in the low half), by the hardware's
+// conversion: round to nearest even, NaN stays NaN.
+typedef __bf16 v2bf_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float a, float b) {
+  const v2bf_t v{(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 }  // namespace mi355moe

@@ -51,13 +51,12 @@ __device__ __forceinline__ void dense_store(const DenseParams& p, typename T::Ac
     }
   } else {
     uint16_t* o = static_cast<uint16_t*>(p.out) + at;
-    uint32_t h[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = f32_to_bf16(f[j]);
+    const uint2 h = make_uint2(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]));
     if (whole && p.out_vec) {
-      *reinterpret_cast<uint2*>(o) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+      *reinterpret_cast<uint2*>(o) = h;
     } else {
-      for (int j = 0; j < 4 && n + j < p.N; ++j) o[j] = (uint16_t)h[j];
+      const uint64_t h4 = ((uint64_t)h.y << 32) | h.x;
+      for (int j = 0; j < 4 && n + j < p.N; ++j) o[j] = (uint16_t)(h4 >> (16 * j));
     }
   }
 }

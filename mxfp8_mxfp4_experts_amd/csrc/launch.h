@@ -117,7 +117,7 @@ struct DenseParams {
   int out_vec;              // rows take 4-element vector stores
   void* partial;            // dense_workspace bytes
 };
-size_t dense_workspace(bool i8, int M, int N, int64_t Kb);
+size_t dense_workspace(int M, int N, int64_t Kb);
 hipError_t launch_dense(bool i8, const DenseParams& p, hipStream_t stream);
 
 }  // namespace mi355moe
