@@ -465,51 +465,71 @@ def moe_prepack_w2(w2, w2_s):
 
 
 # ---------------------------------------------------------------------------
-# Around the experts.  These run a few microseconds each in a decode step, so
-# their checks are kept short: one comparison per property.
+# Around the experts.  In a decode step these kernels run for a few
+# microseconds, so what a call costs on the host counts: the checks below read
+# each property once, and the stream is taken as torch's raw handle.
 
 _BF16, _F32, _U8, _I8, _I32 = (torch.bfloat16, torch.float32, torch.uint8, torch.int8,
                                torch.int32)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t, name, dtype, shape, device):
+def _wrong(t, name, dtype, shape, idx):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor")
+    raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{idx}, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}")
+
+
+def _rows(t, name, dtype, shape, idx):
     """A [T, C] tensor whose rows may be strided; returns its row stride."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+    try:
+        ok = t.dtype is dtype and t.shape == shape and t.get_device() == idx
+    except AttributeError:
+        ok = False
+    if not ok:
+        _wrong(t, name, dtype, shape, idx)
     ld, one = t.stride()
     if one != 1 and shape[1] != 1:
         raise ValueError(f"{name} must have unit column stride")
     return ld if shape[0] > 1 else shape[1]   # the stride of a single row says nothing
 
 
-def _dense(t, name, dtype, shape, device):
-    if t.dtype is not dtype or t.shape != shape or t.device != device:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+def _dense(t, name, dtype, shape, idx):
+    try:
+        ok = t.dtype is dtype and t.shape == shape and t.get_device() == idx
+    except AttributeError:
+        ok = False
+    if not ok:
+        _wrong(t, name, dtype, shape, idx)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
 def _begin(x, name):
-    """The device and its current stream for a call whose main operand is x."""
+    """The device index of a call whose main operand is x, which has to be the
+    current device's."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if x.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
-    dev = x.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {dev}, which is not the current device")
-    return dev, torch.cuda.current_stream().cuda_stream
+    idx = x.get_device()
+    if idx != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {x.device}, which is not the current device")
+    return idx
 
 
-def _workspace(ws, need, dev, name):
+def _new(shape, dtype, idx):
+    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", idx))
+
+
+def _workspace(ws, size_of, sizes, idx):
+    """The given workspace, or a new one of the size that the library names
+    (the library refuses a given one that is too small)."""
     if ws is None:
-        return torch.empty(need, dtype=_U8, device=dev)
-    if ws.dtype is not _U8 or ws.device != dev or not ws.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor on " + str(dev))
-    if ws.numel() < need:
-        raise ValueError(f"{name} needs {need} bytes of workspace, got {ws.numel()}")
+        return _new(size_of(*sizes), _U8, idx)
+    if ws.dtype is not _U8 or ws.get_device() != idx or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{idx}")
     return ws
 
 
@@ -521,35 +541,39 @@ def moe_add_rmsnorm(x, weight, eps: float, residual=None, q8: int = Q8_NONE, res
     and no buffer), and for ``q8`` Q8_MXFP8 uint8 [T, H] and [T, H/32], for
     Q8_INT8 int8 [T, H] and float [T], else None.  ``residual_out`` may be
     ``x`` or ``residual`` itself."""
-    dev, stream = _begin(x, "x")
+    idx = _begin(x, "x")
     shape = x.shape
     T, H = shape
-    ld_x = _rows(x, "x", _BF16, shape, dev)
-    _dense(weight, "weight", _BF16, (H,), dev)
+    ld_x = _rows(x, "x", _BF16, shape, idx)
+    _dense(weight, "weight", _BF16, (H,), idx)
+    r_p = h_p = y_p = q_p = s_p = None
     ld_r = ld_h = ld_y = 0
     if residual is not None:
-        ld_r = _rows(residual, "residual", _BF16, shape, dev)
+        ld_r = _rows(residual, "residual", _BF16, shape, idx)
+        r_p = residual.data_ptr()
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=_BF16, device=dev)
+            residual_out = _new(shape, _BF16, idx)
     if residual_out is not None:
-        ld_h = _rows(residual_out, "residual_out", _BF16, shape, dev)
+        ld_h = _rows(residual_out, "residual_out", _BF16, shape, idx)
+        h_p = residual_out.data_ptr()
     if y is None and want_y:
-        y = torch.empty(shape, dtype=_BF16, device=dev)
+        y = _new(shape, _BF16, idx)
     if y is not None:
-        ld_y = _rows(y, "y", _BF16, shape, dev)
+        ld_y = _rows(y, "y", _BF16, shape, idx)
+        y_p = y.data_ptr()
     if q8 == Q8_MXFP8 or q8 == Q8_INT8:
         kind, s_shape, s_kind = (_U8, (T, H // 32), _U8) if q8 == Q8_MXFP8 else (_I8, (T,), _F32)
         if xq is None:
-            xq = torch.empty(shape, dtype=kind, device=dev)
+            xq = _new(shape, kind, idx)
         if xs is None:
-            xs = torch.empty(s_shape, dtype=s_kind, device=dev)
-        _dense(xq, "xq", kind, shape, dev)
-        _dense(xs, "xs", s_kind, s_shape, dev)
+            xs = _new(s_shape, s_kind, idx)
+        _dense(xq, "xq", kind, shape, idx)
+        _dense(xs, "xs", s_kind, s_shape, idx)
+        q_p, s_p = xq.data_ptr(), xs.data_ptr()
     else:
         xq = xs = None
-    st = lib().moe_add_rmsnorm(x.data_ptr(), ld_x, _ptr(residual), ld_r, weight.data_ptr(), eps, T,
-                               H, q8, _ptr(residual_out), ld_h, _ptr(y), ld_y, _ptr(xq), _ptr(xs),
-                               stream)
+    st = lib().moe_add_rmsnorm(x.data_ptr(), ld_x, r_p, ld_r, weight.data_ptr(), eps, T, H, q8,
+                               h_p, ld_h, y_p, ld_y, q_p, s_p, _raw_stream(idx))
     if st:
         raise MoEError("moe_add_rmsnorm", st)
     return residual_out, y, xq, xs
@@ -557,16 +581,17 @@ def moe_add_rmsnorm(x, weight, eps: float, residual=None, q8: int = Q8_NONE, res
 
 def moe_quant_int8(x, xq=None, xs=None):
     """bf16 rows [T, H] -> int8 [T, H] and one float scale per row [T]."""
-    dev, stream = _begin(x, "x")
-    ld_x = _rows(x, "x", _BF16, x.shape, dev)
+    idx = _begin(x, "x")
     T, H = x.shape
+    ld_x = _rows(x, "x", _BF16, (T, H), idx)
     if xq is None:
-        xq = torch.empty((T, H), dtype=_I8, device=dev)
+        xq = _new((T, H), _I8, idx)
     if xs is None:
-        xs = torch.empty((T,), dtype=_F32, device=dev)
-    _dense(xq, "xq", _I8, (T, H), dev)
-    _dense(xs, "xs", _F32, (T,), dev)
-    st = lib().moe_quant_int8(x.data_ptr(), ld_x, T, H, xq.data_ptr(), xs.data_ptr(), stream)
+        xs = _new((T,), _F32, idx)
+    _dense(xq, "xq", _I8, (T, H), idx)
+    _dense(xs, "xs", _F32, (T,), idx)
+    st = lib().moe_quant_int8(x.data_ptr(), ld_x, T, H, xq.data_ptr(), xs.data_ptr(),
+                              _raw_stream(idx))
     if st:
         raise MoEError("moe_quant_int8", st)
     return xq, xs
@@ -580,40 +605,39 @@ def moe_int8_workspace_size(M: int, N: int, K: int) -> int:
     return n
 
 
-def _int8_out(out, out_dtype, M, N, dev):
+def _int8_out(out, out_dtype, M, N, idx):
     if out is None:
         if out_dtype not in _OUT_TYPE:
             raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = _new((M, N), out_dtype, idx)
     elif out.dtype not in _OUT_TYPE:
         raise ValueError(f"out must be bfloat16 or float32, got {out.dtype}")
-    return out, _rows(out, "out", out.dtype, (M, N), dev), _OUT_TYPE[out.dtype]
+    return out, _rows(out, "out", out.dtype, (M, N), idx), _OUT_TYPE[out.dtype]
 
 
-def _int8_weight(w, w_s, K, dev):
+def _int8_weight(w, w_s, K, idx):
     if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"w must be [N, {K}]")
     N = w.shape[0]
-    _dense(w, "w", _I8, (N, K), dev)
-    _dense(w_s, "w_s", _F32, (N,), dev)
+    _dense(w, "w", _I8, (N, K), idx)
+    _dense(w_s, "w_s", _F32, (N,), idx)
     return N
 
 
 def moe_int8_matmul(xq, xs, w, w_s, out=None, out_dtype=torch.bfloat16, workspace=None):
     """out [M, N] = (xq [M, K] . w [N, K]) * xs [M] * w_s [N], the sum exact in
     int32; ``out`` or ``out_dtype`` says bf16 or float32."""
-    dev, stream = _begin(xq, "xq")
+    idx = _begin(xq, "xq")
     M, K = xq.shape
-    ld_xq = _rows(xq, "xq", _I8, xq.shape, dev)
-    _dense(xs, "xs", _F32, (M,), dev)
-    N = _int8_weight(w, w_s, K, dev)
-    out, ld_out, kind = _int8_out(out, out_dtype, M, N, dev)
+    ld_xq = _rows(xq, "xq", _I8, (M, K), idx)
+    _dense(xs, "xs", _F32, (M,), idx)
+    N = _int8_weight(w, w_s, K, idx)
+    out, ld_out, kind = _int8_out(out, out_dtype, M, N, idx)
     L = lib()
-    workspace = _workspace(workspace, L.moe_int8_workspace_size(M, N, K) if workspace is None
-                           else 0, dev, "moe_int8_matmul")
+    workspace = _workspace(workspace, L.moe_int8_workspace_size, (M, N, K), idx)
     st = L.moe_int8_matmul(xq.data_ptr(), ld_xq, xs.data_ptr(), w.data_ptr(), w_s.data_ptr(), M, N,
                            K, kind, out.data_ptr(), ld_out, workspace.data_ptr(),
-                           workspace.numel(), stream)
+                           workspace.numel(), _raw_stream(idx))
     if st:
         raise MoEError("moe_int8_matmul", st)
     return out
@@ -621,16 +645,16 @@ def moe_int8_matmul(xq, xs, w, w_s, out=None, out_dtype=torch.bfloat16, workspac
 
 def moe_int8_linear(x, w, w_s, out=None, out_dtype=torch.bfloat16, workspace=None):
     """moe_quant_int8 of x [M, K] (bf16) and moe_int8_matmul as one call."""
-    dev, stream = _begin(x, "x")
+    idx = _begin(x, "x")
     M, K = x.shape
-    ld_x = _rows(x, "x", _BF16, x.shape, dev)
-    N = _int8_weight(w, w_s, K, dev)
-    out, ld_out, kind = _int8_out(out, out_dtype, M, N, dev)
+    ld_x = _rows(x, "x", _BF16, (M, K), idx)
+    N = _int8_weight(w, w_s, K, idx)
+    out, ld_out, kind = _int8_out(out, out_dtype, M, N, idx)
     L = lib()
-    workspace = _workspace(workspace, L.moe_int8_workspace_size(M, N, K) if workspace is None
-                           else 0, dev, "moe_int8_linear")
+    workspace = _workspace(workspace, L.moe_int8_workspace_size, (M, N, K), idx)
     st = L.moe_int8_linear(x.data_ptr(), ld_x, w.data_ptr(), w_s.data_ptr(), M, N, K, kind,
-                           out.data_ptr(), ld_out, workspace.data_ptr(), workspace.numel(), stream)
+                           out.data_ptr(), ld_out, workspace.data_ptr(), workspace.numel(),
+                           _raw_stream(idx))
     if st:
         raise MoEError("moe_int8_linear", st)
     return out
@@ -643,21 +667,20 @@ def moe_gate_workspace_size(T: int, E: int, H: int) -> int:
 
 def moe_gate_logits(x, w, out=None, workspace=None):
     """Router logits float [T, E] of x [T, H] and w [E, H], both bf16."""
-    dev, stream = _begin(x, "x")
+    idx = _begin(x, "x")
     T, H = x.shape
-    ld_x = _rows(x, "x", _BF16, x.shape, dev)
+    ld_x = _rows(x, "x", _BF16, (T, H), idx)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError(f"w must be [E, {H}]")
     E = w.shape[0]
-    _dense(w, "w", _BF16, (E, H), dev)
+    _dense(w, "w", _BF16, (E, H), idx)
     if out is None:
-        out = torch.empty((T, E), dtype=_F32, device=dev)
-    ld_out = _rows(out, "out", _F32, (T, E), dev)
+        out = _new((T, E), _F32, idx)
+    ld_out = _rows(out, "out", _F32, (T, E), idx)
     L = lib()
-    workspace = _workspace(workspace, L.moe_gate_workspace_size(T, E, H) if workspace is None
-                           else 0, dev, "moe_gate_logits")
+    workspace = _workspace(workspace, L.moe_gate_workspace_size, (T, E, H), idx)
     st = L.moe_gate_logits(x.data_ptr(), ld_x, w.data_ptr(), T, E, H, out.data_ptr(), ld_out,
-                           workspace.data_ptr(), workspace.numel(), stream)
+                           workspace.data_ptr(), workspace.numel(), _raw_stream(idx))
     if st:
         raise MoEError("moe_gate_logits", st)
     return out
@@ -671,21 +694,23 @@ def moe_route_groups(logits, bias, top_k: int, n_group: int = 1, topk_group: int
     weights float [T, top_k]; -1 with weight 0 where no unmasked expert is
     left.  ``score``: SCORE_SIGMOID or SCORE_SOFTMAX; ``group_score``:
     GROUP_MAX or GROUP_TOP2."""
-    dev, stream = _begin(logits, "logits")
+    idx = _begin(logits, "logits")
     T, E = logits.shape
-    ld = _rows(logits, "logits", _F32, logits.shape, dev)
+    ld = _rows(logits, "logits", _F32, (T, E), idx)
+    b_p = None
     if bias is not None:
-        _dense(bias, "bias", _F32, (E,), dev)
+        _dense(bias, "bias", _F32, (E,), idx)
+        b_p = bias.data_ptr()
     shape = (T, top_k)
     if topk_idx is None:
-        topk_idx = torch.empty(shape, dtype=_I32, device=dev)
+        topk_idx = _new(shape, _I32, idx)
     if topk_w is None:
-        topk_w = torch.empty(shape, dtype=_F32, device=dev)
-    _dense(topk_idx, "topk_idx", _I32, shape, dev)
-    _dense(topk_w, "topk_w", _F32, shape, dev)
-    st = lib().moe_route_groups(logits.data_ptr(), ld, _ptr(bias), T, E, top_k, n_group,
-                                topk_group, score, group_score, 1 if renormalise else 0,
-                                routed_scaling, topk_idx.data_ptr(), topk_w.data_ptr(), stream)
+        topk_w = _new(shape, _F32, idx)
+    _dense(topk_idx, "topk_idx", _I32, shape, idx)
+    _dense(topk_w, "topk_w", _F32, shape, idx)
+    st = lib().moe_route_groups(logits.data_ptr(), ld, b_p, T, E, top_k, n_group, topk_group,
+                                score, group_score, 1 if renormalise else 0, routed_scaling,
+                                topk_idx.data_ptr(), topk_w.data_ptr(), _raw_stream(idx))
     if st:
         raise MoEError("moe_route_groups", st)
     return topk_idx, topk_w
