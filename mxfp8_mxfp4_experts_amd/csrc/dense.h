@@ -13,6 +13,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 struct DenseI8 {
   using Acc = v4i;
+  using Elem = int;
   static constexpr bool kInt = true;
   static __device__ __forceinline__ Acc mfma(v4i a, v4i b, Acc c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
@@ -20,6 +21,7 @@ struct DenseI8 {
 };
 struct DenseBf16 {
   using Acc = v4f;
+  using Elem = float;
   static constexpr bool kInt = false;
   static __device__ __forceinline__ Acc mfma(v4i a, v4i b, Acc c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),

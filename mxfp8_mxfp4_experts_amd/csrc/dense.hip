@@ -12,60 +12,200 @@
 #include "dense.h"
 #include "dense_tile.h"
 #include "launch.h"
+#include "q8_dev.h"
 
 namespace mi355moe {
 
 namespace {
 
-// Few rows: no operand is used twice enough to pay for LDS.  A workgroup owns
-// 16 output columns and 16 MI tokens; its W wavefronts split K (64 bytes in
-// turn, so together they read runs of 64 W bytes of each weight row), each
-// feeding the matrix unit straight from global loads, and the partial tiles
-// are added through LDS in wavefront order.
-template <class T, int MI, int W>
-__global__ __launch_bounds__(64 * W) void dense_direct_kernel(DenseParams p) {
+// Few rows: no operand is used twice enough to pay for LDS.  A workgroup of W
+// wavefronts owns 16 / Q output columns and 16 / Q tokens and splits K over its
+// wavefronts, each feeding the matrix unit straight from global loads, with the
+// loads of kBatch steps in flight; the partial tiles are added through LDS in
+// wavefront order.
+//
+// Q: a 16x16 tile of 16 columns x 16 tokens is mostly empty for one to eight
+// tokens, and N / 16 workgroups are too few to draw on the whole chip's
+// bandwidth.  With Q > 1 the tile's rows are (column, kq) and its columns
+// (token, kq), where kq < Q says which of Q neighbouring 64-byte pieces of K
+// the row or column carries: the products with equal kq on both sides are the
+// sums wanted, the others are not read.  So a workgroup covers 16 / Q columns at
+// Q times the length of K per step, and a launch has Q times the workgroups.
+constexpr int kDirectWaves = 16;
+constexpr int kBatch = 8;
+
+template <class T, int Q>
+struct DirectGeom {
+  static constexpr int kCols = 16 / Q;              // output columns, and tokens
+  static constexpr int kStep = 64 * Q * kDirectWaves;   // bytes of K per step
+};
+
+// Adds the wavefronts' tiles and stores the workgroup's outputs.
+template <class T, int Q>
+__device__ __forceinline__ void direct_finish(const DenseParams& p, typename T::Acc acc, int m0,
+                                              int n0, typename T::Acc* red_s) {
   using Acc = typename T::Acc;
-  __shared__ Acc red_s[W][MI][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MI;
-  const uint8_t* bp = p.b + (int64_t)min(n0 + r, p.N - 1) * p.ld_b + 16 * g;
-  const uint8_t* ap[MI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-    ap[i] = p.a + (int64_t)min(m0 + 16 * i + r, p.M - 1) * p.ld_a + 16 * g;
-  Acc acc[MI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i) acc[i] = Acc{0, 0, 0, 0};
-  const int Kb = p.Kb;
-#pragma unroll 4
-  for (int k = 64 * wave; k < Kb; k += 64 * W) {
-    const bool in = k + 16 * g < Kb;   // K is whole 16-byte pieces
-    const v4i zero{0, 0, 0, 0};
-    const v4i b = in ? *reinterpret_cast<const v4i*>(bp + k) : zero;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const v4i a = in ? *reinterpret_cast<const v4i*>(ap[i] + k) : zero;
-      acc[i] = T::mfma(b, a, acc[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < MI; ++i) red_s[wave][i][lane] = acc[i];
+  using E = typename T::Elem;
+  constexpr int C = 16 / Q;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tid = threadIdx.x;
+  red_s[64 * wave + lane] = acc;
   __syncthreads();
-  for (int j = threadIdx.x; j < 64 * MI; j += 64 * W) {
-    const int i = j >> 6, l = j & 63;
-    Acc s = red_s[0][i][l];
+  if constexpr (Q == 1) {
+    if (tid < 64) {
+      Acc s = red_s[lane];
 #pragma unroll
-    for (int w = 1; w < W; ++w) s += red_s[w][i][l];
-    dense_store<T>(p, s, m0 + 16 * i + (l & 15), n0 + 4 * (l >> 4));
+      for (int w = 1; w < kDirectWaves; ++w) s += red_s[64 * w + lane];
+      dense_store<T>(p, s, m0 + (lane & 15), n0 + 4 * (lane >> 4));
+    }
+  } else {
+    // Entry e of a wavefront's tile: lane e / 4, element e % 4 -- row 4 (lane / 16)
+    // + e % 4, column lane % 16.  One thread per output: its Q entries on the
+    // diagonal, wavefront by wavefront.
+    const E* red = reinterpret_cast<const E*>(red_s);
+    if (tid < C * C) {
+      const int c = tid % C, m = tid / C;
+      E s = 0;
+#pragma unroll
+      for (int kq = 0; kq < Q; ++kq) {
+        const int row = c * Q + kq, col = m * Q + kq;
+        const int e = 4 * (16 * (row >> 2) + col) + (row & 3);
+#pragma unroll
+        for (int w = 0; w < kDirectWaves; ++w) s += red[256 * w + e];
+      }
+      if (m0 + m < p.M && n0 + c < p.N) {
+        float f = (float)s;
+        if constexpr (T::kInt) f = f * p.sx[m0 + m] * p.sw[n0 + c];
+        const int64_t at = (int64_t)(m0 + m) * p.ld_out + n0 + c;
+        if (p.out_f32)
+          static_cast<float*>(p.out)[at] = f;
+        else
+          static_cast<uint16_t*>(p.out)[at] = (uint16_t)f32x2_to_bf16x2(f, 0.0f);
+      }
+    }
   }
 }
 
-template <class T, int MI, int W>
+template <class T, int Q>
+__global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_kernel(DenseParams p) {
+  using Acc = typename T::Acc;
+  using G = DirectGeom<T, Q>;
+  __shared__ Acc red_s[64 * kDirectWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = (lane & 15) / Q, kq = lane % Q, g = lane >> 4;
+  const int n0 = blockIdx.x * G::kCols, m0 = blockIdx.y * G::kCols;
+  const int k0 = 64 * (Q * wave + kq) + 16 * g;    // K is whole 16-byte pieces
+  const uint8_t* bp = p.b + (int64_t)min(n0 + c, p.N - 1) * p.ld_b + k0;
+  const uint8_t* ap = p.a + (int64_t)min(m0 + c, p.M - 1) * p.ld_a + k0;
+  const int left = p.Kb - k0;
+  const v4i zero{0, 0, 0, 0};
+  Acc acc{0, 0, 0, 0};
+  for (int k = 0; k < p.Kb; k += kBatch * G::kStep) {
+    v4i a[kBatch], b[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int at = k + i * G::kStep;
+      b[i] = at < left ? *reinterpret_cast<const v4i*>(bp + at) : zero;
+      a[i] = at < left ? *reinterpret_cast<const v4i*>(ap + at) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) acc = T::mfma(b[i], a[i], acc);
+  }
+  direct_finish<T, Q>(p, acc, m0, n0, red_s);
+}
+
+// INT8 with bf16 tokens, in one launch: the workgroup quantises its tokens (at
+// most 16 / Q, with the rule of moe_quant_int8) into LDS while its first weight
+// loads are on their way.
+template <int Q>
+__global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_quant_kernel(
+    DenseParams p, const uint16_t* __restrict__ x, int64_t ld_x) {
+  using T = DenseI8;
+  using G = DirectGeom<T, Q>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t tok_s[];   // [M][K + 16]
+  __shared__ v4i red_s[64 * kDirectWaves];
+  __shared__ uint32_t max_s[16 / Q][kDirectWaves];
+  __shared__ float sx_s[16 / Q];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int c = (lane & 15) / Q, kq = lane % Q, g = lane >> 4;
+  const int n0 = blockIdx.x * G::kCols, K = p.Kb, M = p.M, pieces = K / 8, row_s = K + 16;
+  const int k0 = 64 * (Q * wave + kq) + 16 * g;
+  const uint8_t* bp = p.b + (int64_t)min(n0 + c, p.N - 1) * p.ld_b + k0;
+  const int left = K - k0;
+  const v4i zero{0, 0, 0, 0};
+  v4i b[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i)
+    b[i] = i * G::kStep < left ? *reinterpret_cast<const v4i*>(bp + i * G::kStep) : zero;
+
+  // Absolute maxima (as bits: a NaN counts as the largest).
+  for (int m = 0; m < M; ++m) {
+    uint32_t top = 0;
+    for (int q = tid; q < pieces; q += 64 * kDirectWaves) {
+      const uint4 v = reinterpret_cast<const uint4*>(x + m * ld_x)[q];
+      top = max(top, absmax8_bits(v));
+    }
+    top = wave_umax(top);
+    if (lane == 0) max_s[m][wave] = top;
+  }
+  __syncthreads();
+  for (int m = 0; m < M; ++m) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int w = 0; w < kDirectWaves; ++w) top = max(top, max_s[m][w]);
+    const Int8Scale s = int8_scale(__uint_as_float(top));
+    if (tid == 0) sx_s[m] = s.scale;
+    for (int q = tid; q < pieces; q += 64 * kDirectWaves) {
+      float f[8];
+      unpack8(reinterpret_cast<const uint4*>(x + m * ld_x)[q], f);
+      *reinterpret_cast<uint2*>(tok_s + m * row_s + 8 * q) = int8x8(f, s);
+    }
+  }
+  __syncthreads();
+
+  const uint8_t* ap = tok_s + min(c, M - 1) * row_s + k0;
+  v4i acc = zero;
+  for (int k = 0; k < K; k += kBatch * G::kStep) {
+    v4i next[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int at = k + (kBatch + i) * G::kStep;
+      next[i] = at < left ? *reinterpret_cast<const v4i*>(bp + at) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int at = k + i * G::kStep;
+      const v4i a = at < left ? *reinterpret_cast<const v4i*>(ap + at) : zero;
+      acc = T::mfma(b[i], a, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) b[i] = next[i];
+  }
+  p.sx = sx_s;
+  direct_finish<T, Q>(p, acc, 0, n0, red_s);
+}
+
+// Q for M tokens and N columns: as many workgroups as bring the chip to its
+// bandwidth (about one per CU), as far as the tokens leave room.
+int direct_q(int M, int N) {
+  int q = 1;
+  while (q < 4 && M <= 16 / (2 * q) && (N * (int64_t)q + 15) / 16 < 224) q *= 2;
+  return q;
+}
+
+template <class T, int Q>
 hipError_t direct(const DenseParams& p, hipStream_t stream) {
-  const dim3 grid((p.N + 15) / 16, (p.M + 16 * MI - 1) / (16 * MI));
-  hipLaunchKernelGGL((dense_direct_kernel<T, MI, W>), grid, dim3(64 * W), 0, stream, p);
+  constexpr int C = 16 / Q;
+  const dim3 grid((p.N + C - 1) / C, (p.M + C - 1) / C);
+  hipLaunchKernelGGL((dense_direct_kernel<T, Q>), grid, dim3(64 * kDirectWaves), 0, stream, p);
   return hipGetLastError();
+}
+template <class T>
+hipError_t direct(const DenseParams& p, hipStream_t stream) {
+  switch (direct_q(p.M, p.N)) {
+    case 1: return direct<T, 1>(p, stream);
+    case 2: return direct<T, 2>(p, stream);
+    default: return direct<T, 4>(p, stream);
+  }
 }
 
 // The tiled kernel's variants, widest tile first: what one stage takes with at
@@ -85,6 +225,8 @@ constexpr int kNumVariants = sizeof(kVariants) / sizeof(kVariants[0]);
 constexpr int kCus = 256;
 constexpr int kMaxSplits = 16;
 constexpr int kDirectRows = 16;
+constexpr int kFusedRows = 8;          // tokens that the one-launch INT8 call quantises itself
+constexpr int kFusedBytes = 44 << 10;  // their codes in LDS, next to 16 KB of partial tiles
 
 struct Pick {
   int variant;   // -1: the direct kernel
@@ -127,7 +269,7 @@ hipError_t launch(const DenseParams& p, hipStream_t stream) {
   // apart than that take the direct kernel, whose addresses are 64-bit.
   const int64_t ld = p.ld_a > p.ld_b ? p.ld_a : p.ld_b;
   if (k.variant < 0 || 256 * ld + p.Kb >= (int64_t)1 << 31)
-    return p.M <= kDirectRows ? direct<T, 1, 16>(p, stream) : direct<T, 4, 4>(p, stream);
+    return direct<T>(p, stream);
   switch (k.variant) {
     case 0: return dense_tile_launch<T, 2, 2, 8, 7, 2, 1>(p, k.splits, stream);
     case 1: return dense_tile_launch<T, 2, 2, 4, 7, 3, 1>(p, k.splits, stream);
@@ -147,6 +289,30 @@ size_t dense_workspace(int M, int N, int64_t Kb) {
   const Pick k = pick(M, N, Kb);
   if (k.variant < 0 || k.splits == 1) return 0;
   return (size_t)k.splits * M * ((N + 3) / 4 * 4) * 4;
+}
+
+bool dense_fuses_quant(int M, int N, int K) {
+  return M <= kFusedRows && (int64_t)M * (K + 16) <= kFusedBytes && M <= 16 / direct_q(M, N);
+}
+
+hipError_t launch_dense_quant(const DenseParams& p, const uint16_t* x, int64_t ld_x,
+                              hipStream_t stream) {
+  const size_t lds = (size_t)p.M * (p.Kb + 16);
+  const dim3 block(64 * kDirectWaves);
+  switch (direct_q(p.M, p.N)) {
+    case 1:
+      hipLaunchKernelGGL((dense_direct_quant_kernel<1>), dim3((p.N + 15) / 16), block, lds, stream,
+                         p, x, ld_x);
+      break;
+    case 2:
+      hipLaunchKernelGGL((dense_direct_quant_kernel<2>), dim3((p.N + 7) / 8), block, lds, stream,
+                         p, x, ld_x);
+      break;
+    default:
+      hipLaunchKernelGGL((dense_direct_quant_kernel<4>), dim3((p.N + 3) / 4), block, lds, stream,
+                         p, x, ld_x);
+  }
+  return hipGetLastError();
 }
 
 hipError_t launch_dense(bool i8, const DenseParams& p, hipStream_t stream) {

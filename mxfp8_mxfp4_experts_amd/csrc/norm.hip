@@ -14,86 +14,12 @@
 // largest |h * w| times rstd exactly, and the sum of squares and the absolute
 // maximum are reduced together with one barrier.
 #include "common.h"
-#include "fc_common.h"   // e4m3x4_scaled
 #include "launch.h"
+#include "q8_dev.h"
 
 namespace mi355moe {
 
 namespace {
-
-constexpr float kMinScale = 1.17549435e-38f;   // 2^-126: 1 / s stays finite
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
-}
-// NaN counts as the largest value: a row that holds one must not hide it.
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)v, off);
-    v = o > v ? o : v;
-  }
-  return v;
-}
-
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
-    f[2 * i + 1] = bf16_to_f32(w[i] >> 16);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16(f[2 * i]) | (f32_to_bf16(f[2 * i + 1]) << 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Whole numbers of [-127, 127] of 8 values; inv = 1 / s.
-__device__ __forceinline__ uint2 int8x8(const float (&f)[8], float inv) {
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float r = fminf(fmaxf(__builtin_rintf(f[i] * inv), -127.0f), 127.0f);
-    w[i >> 2] |= ((uint32_t)(int)r & 0xFFu) << (8 * (i & 3));
-  }
-  return make_uint2(w[0], w[1]);
-}
-
-// MXFP8 codes of a lane's 8 values and its 32-element group's scale byte;
-// the group is four consecutive lanes.
-__device__ __forceinline__ uint2 mxfp8x8(const float (&f)[8], uint32_t& scale) {
-  float amax = 0.0f;
-  uint32_t odd = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = fabsf(f[i]);
-    amax = a > amax ? a : amax;   // NaN compares false: ignored
-    odd |= (__float_as_uint(f[i]) & 0x7F800000u) == 0x7F800000u;
-  }
-  amax = fmaxf(amax, __shfl_xor(amax, 1));
-  amax = fmaxf(amax, __shfl_xor(amax, 2));
-  odd |= __shfl_xor(odd, 1);
-  odd |= __shfl_xor(odd, 2);
-  const int e = mx8_exponent(amax);
-  scale = (uint32_t)(e + 127);
-  uint32_t lo = 0, hi = 0;
-  if (!odd && e > -127) {
-    const float s2 = __uint_as_float((uint32_t)(e + 127) << 23);
-    lo = e4m3x4_scaled(f[0], f[1], f[2], f[3], s2);
-    hi = e4m3x4_scaled(f[4], f[5], f[6], f[7], s2);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lo |= e4m3_encode(ldexpf(f[i], -e)) << (8 * i);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) hi |= e4m3_encode(ldexpf(f[4 + i], -e)) << (8 * i);
-  }
-  return make_uint2(lo, hi);
-}
 
 // One row per workgroup, P 8-element pieces per thread (piece tid + i *
 // blockDim).  NORM false: y = x (the 8-bit quantisation alone).
@@ -165,14 +91,10 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
     if constexpr (Q8 == MOE_Q8_INT8) top = max_s[i] > top ? max_s[i] : top;
   }
   const float rstd = NORM ? 1.0f / sqrtf(sum / (float)p.H + p.eps) : 1.0f;
-  float inv = 0.0f;
-  bool odd = false;
+  Int8Scale s8;
   if constexpr (Q8 == MOE_Q8_INT8) {
-    const float amax = NORM ? __uint_as_float(top) * rstd : __uint_as_float(top);
-    odd = !(amax <= 3.402823466e38f);   // the row holds an infinity or a NaN
-    const float s = fmaxf(amax / 127.0f, kMinScale);
-    inv = 1.0f / s;
-    if (tid == 0) reinterpret_cast<float*>(p.xs)[row] = odd ? __uint_as_float(0x7FC00000u) : s;
+    s8 = int8_scale(NORM ? __uint_as_float(top) * rstd : __uint_as_float(top));
+    if (tid == 0) reinterpret_cast<float*>(p.xs)[row] = s8.scale;
   }
 #pragma unroll
   for (int i = 0; i < P; ++i) {
@@ -185,7 +107,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
       if (p.y) reinterpret_cast<uint4*>(p.y + row * p.ld_y)[c] = pack8(f[i]);
     }
     if constexpr (Q8 == MOE_Q8_INT8) {
-      reinterpret_cast<uint2*>(p.xq + row * p.H)[c] = odd ? make_uint2(0, 0) : int8x8(f[i], inv);
+      reinterpret_cast<uint2*>(p.xq + row * p.H)[c] = int8x8(f[i], s8);
     }
     if constexpr (Q8 == MOE_Q8_MXFP8) {
       uint32_t scale;
