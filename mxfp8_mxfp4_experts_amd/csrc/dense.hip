@@ -21,7 +21,7 @@ namespace {
 // Few rows: no operand is used twice enough to pay for LDS.  A workgroup of W
 // wavefronts owns 16 / Q output columns and 16 / Q tokens and splits K over its
 // wavefronts, each feeding the matrix unit straight from global loads, with the
-// loads of kBatch steps in flight; the partial tiles are added through LDS in
+// loads of several steps in flight; the partial tiles are added through LDS in
 // wavefront order.
 //
 // Q: a 16x16 tile of 16 columns x 16 tokens is mostly empty for one to eight
@@ -32,7 +32,7 @@ namespace {
 // sums wanted, the others are not read.  So a workgroup covers 16 / Q columns at
 // Q times the length of K per step, and a launch has Q times the workgroups.
 constexpr int kDirectWaves = 16;
-constexpr int kBatch = 8;
+constexpr int kFusedUnits = 4;         // units of 512 elements a wavefront quantises
 
 template <class T, int Q>
 struct DirectGeom {
@@ -85,7 +85,9 @@ __device__ __forceinline__ void direct_finish(const DenseParams& p, typename T::
   }
 }
 
-template <class T, int Q>
+// kHalf steps' loads at once, twice; MORE: K is longer than that.  Short rows take
+// the small batches, whose registers let two workgroups share a CU.
+template <class T, int Q, int kHalf, bool MORE>
 __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_kernel(DenseParams p) {
   using Acc = typename T::Acc;
   using G = DirectGeom<T, Q>;
@@ -97,18 +99,37 @@ __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_kernel(DensePa
   const uint8_t* bp = p.b + (int64_t)min(n0 + c, p.N - 1) * p.ld_b + k0;
   const uint8_t* ap = p.a + (int64_t)min(m0 + c, p.M - 1) * p.ld_a + k0;
   const int left = p.Kb - k0;
-  const v4i zero{0, 0, 0, 0};
   Acc acc{0, 0, 0, 0};
-  for (int k = 0; k < p.Kb; k += kBatch * G::kStep) {
-    v4i a[kBatch], b[kBatch];
+  // With MORE the halves take turns: one's matrix instructions while the other is
+  // on its way.
+  struct Batch {
+    v4i a[kHalf], b[kHalf];
+  } one, two;
+  auto load = [&](Batch& s, int k) __attribute__((always_inline)) {
+    const v4i zero{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < kHalf; ++i) {
       const int at = k + i * G::kStep;
-      b[i] = at < left ? *reinterpret_cast<const v4i*>(bp + at) : zero;
-      a[i] = at < left ? *reinterpret_cast<const v4i*>(ap + at) : zero;
+      s.b[i] = at < left ? *reinterpret_cast<const v4i*>(bp + at) : zero;
+      s.a[i] = at < left ? *reinterpret_cast<const v4i*>(ap + at) : zero;
     }
+  };
+  auto use = [&](const Batch& s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) acc = T::mfma(b[i], a[i], acc);
+    for (int i = 0; i < kHalf; ++i) acc = T::mfma(s.b[i], s.a[i], acc);
+  };
+  load(one, 0);
+  load(two, kHalf * G::kStep);
+  if constexpr (!MORE) {
+    use(one);
+    use(two);
+  } else {
+    for (int k = 0; k < p.Kb; k += 2 * kHalf * G::kStep) {
+      use(one);
+      load(one, k + 2 * kHalf * G::kStep);
+      use(two);
+      load(two, k + 3 * kHalf * G::kStep);
+    }
   }
   direct_finish<T, Q>(p, acc, m0, n0, red_s);
 }
@@ -116,18 +137,19 @@ __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_kernel(DensePa
 // INT8 with bf16 tokens, in one launch: the workgroup quantises its tokens (at
 // most 16 / Q, with the rule of moe_quant_int8) into LDS while its first weight
 // loads are on their way.
-template <int Q>
+template <int Q, int kBatch>
 __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_quant_kernel(
     DenseParams p, const uint16_t* __restrict__ x, int64_t ld_x) {
   using T = DenseI8;
   using G = DirectGeom<T, Q>;
   extern __shared__ __attribute__((aligned(16))) uint8_t tok_s[];   // [M][K + 16]
   __shared__ v4i red_s[64 * kDirectWaves];
-  __shared__ uint32_t max_s[16 / Q][kDirectWaves];
+  __shared__ uint32_t max_s[kFusedUnits * kDirectWaves];
   __shared__ float sx_s[16 / Q];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = (lane & 15) / Q, kq = lane % Q, g = lane >> 4;
   const int n0 = blockIdx.x * G::kCols, K = p.Kb, M = p.M, pieces = K / 8, row_s = K + 16;
+  const int units = (pieces + 63) / 64;
   const int k0 = 64 * (Q * wave + kq) + 16 * g;
   const uint8_t* bp = p.b + (int64_t)min(n0 + c, p.N - 1) * p.ld_b + k0;
   const int left = K - k0;
@@ -137,26 +159,34 @@ __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_quant_kernel(
   for (int i = 0; i < kBatch; ++i)
     b[i] = i * G::kStep < left ? *reinterpret_cast<const v4i*>(bp + i * G::kStep) : zero;
 
-  // Absolute maxima (as bits: a NaN counts as the largest).
-  for (int m = 0; m < M; ++m) {
-    uint32_t top = 0;
-    for (int q = tid; q < pieces; q += 64 * kDirectWaves) {
-      const uint4 v = reinterpret_cast<const uint4*>(x + m * ld_x)[q];
-      top = max(top, absmax8_bits(v));
-    }
-    top = wave_umax(top);
-    if (lane == 0) max_s[m][wave] = top;
+  // Units of 512 elements of a token: wavefront w takes units w, w + 16, ..., all
+  // their loads at once, and leaves each unit's absolute maximum (as bits: a NaN
+  // counts as the largest).
+  uint4 xv[kFusedUnits];
+#pragma unroll
+  for (int i = 0; i < kFusedUnits; ++i) {
+    const int u = wave + kDirectWaves * i, m = u / units, q = 64 * (u - m * units) + lane;
+    xv[i] = m < M && q < pieces ? reinterpret_cast<const uint4*>(x + m * ld_x)[q]
+                                : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < kFusedUnits; ++i) {
+    if (wave + kDirectWaves * i >= M * units) break;
+    const uint32_t top = wave_umax(absmax8_bits(xv[i]));
+    if (lane == 0) max_s[wave + kDirectWaves * i] = top;
   }
   __syncthreads();
-  for (int m = 0; m < M; ++m) {
-    uint32_t top = 0;
 #pragma unroll
-    for (int w = 0; w < kDirectWaves; ++w) top = max(top, max_s[m][w]);
+  for (int i = 0; i < kFusedUnits; ++i) {
+    const int u = wave + kDirectWaves * i, m = u / units, q = 64 * (u - m * units) + lane;
+    if (m >= M) break;
+    uint32_t top = 0;
+    for (int j = 0; j < units; ++j) top = max(top, max_s[m * units + j]);
     const Int8Scale s = int8_scale(__uint_as_float(top));
-    if (tid == 0) sx_s[m] = s.scale;
-    for (int q = tid; q < pieces; q += 64 * kDirectWaves) {
+    if (q == 0) sx_s[m] = s.scale;
+    if (q < pieces) {
       float f[8];
-      unpack8(reinterpret_cast<const uint4*>(x + m * ld_x)[q], f);
+      unpack8(xv[i], f);
       *reinterpret_cast<uint2*>(tok_s + m * row_s + 8 * q) = int8x8(f, s);
     }
   }
@@ -184,11 +214,34 @@ __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_quant_kernel(
   direct_finish<T, Q>(p, acc, 0, n0, red_s);
 }
 
-// Q for M tokens and N columns: as many workgroups as bring the chip to its
-// bandwidth (about one per CU), as far as the tokens leave room.
-int direct_q(int M, int N) {
+// Estimated time of the direct kernel, in ns: a workgroup reads its columns and
+// its tokens, a CU about 64 bytes/ns where a load instruction takes whole 128-byte
+// lines (Q of 2 or 4) and 37 where it takes half lines, the chip its weights at
+// about 5600 bytes/ns; the first loads and the join take about 2 us at least.
+// (Router product of 32 tokens, 896 x 7168: 14.9 us with Q = 1, 9.5 with 2; INT8
+// 16 x 3584 x 7168: 8.7 us with 1, 11.2 with 2.)
+constexpr int kCus = 256;
+float direct_ns(int q, int M, int N, int64_t Kb) {
+  const int c = 16 / q;
+  const int64_t wgs = (int64_t)((N + c - 1) / c) * ((M + c - 1) / c);
+  const float per_cu = (float)((wgs + kCus - 1) / kCus) * (c + (M < c ? M : c)) * Kb /
+                       (q == 1 ? 37.0f : 64.0f);
+  const float chip = (float)N * Kb / 5600.0f;
+  const float t = per_cu > chip ? per_cu : chip;
+  return t > 2000.0f ? t : 2000.0f;
+}
+// The Q of least estimated time.
+int direct_q(int M, int N, int64_t Kb) {
+  int best = 1;
+  for (int q = 2; q <= 4; q *= 2)
+    if (direct_ns(q, M, N, Kb) < direct_ns(best, M, N, Kb)) best = q;
+  return best;
+}
+// For tokens quantised in the same launch: every workgroup quantises all of them,
+// so no more workgroups than CUs where N allows it.
+int fused_q(int M, int N) {
   int q = 1;
-  while (q < 4 && M <= 16 / (2 * q) && (N * (int64_t)q + 15) / 16 < 224) q *= 2;
+  while (q < 4 && M <= 8 / q && (N * (int64_t)(2 * q) + 15) / 16 <= kCus) q *= 2;
   return q;
 }
 
@@ -196,16 +249,39 @@ template <class T, int Q>
 hipError_t direct(const DenseParams& p, hipStream_t stream) {
   constexpr int C = 16 / Q;
   const dim3 grid((p.N + C - 1) / C, (p.M + C - 1) / C);
-  hipLaunchKernelGGL((dense_direct_kernel<T, Q>), grid, dim3(64 * kDirectWaves), 0, stream, p);
+  const dim3 block(64 * kDirectWaves);
+  const int steps = (p.Kb + DirectGeom<T, Q>::kStep - 1) / DirectGeom<T, Q>::kStep;
+  if (steps <= 2)
+    hipLaunchKernelGGL((dense_direct_kernel<T, Q, 1, false>), grid, block, 0, stream, p);
+  else if (steps <= 4)
+    hipLaunchKernelGGL((dense_direct_kernel<T, Q, 2, false>), grid, block, 0, stream, p);
+  else if (steps <= 8)
+    hipLaunchKernelGGL((dense_direct_kernel<T, Q, 4, false>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((dense_direct_kernel<T, Q, 4, true>), grid, block, 0, stream, p);
   return hipGetLastError();
 }
 template <class T>
 hipError_t direct(const DenseParams& p, hipStream_t stream) {
-  switch (direct_q(p.M, p.N)) {
+  switch (direct_q(p.M, p.N, p.Kb)) {
     case 1: return direct<T, 1>(p, stream);
     case 2: return direct<T, 2>(p, stream);
     default: return direct<T, 4>(p, stream);
   }
+}
+
+template <int Q>
+hipError_t direct_quant(const DenseParams& p, const uint16_t* x, int64_t ld_x,
+                        hipStream_t stream) {
+  constexpr int C = 16 / Q;
+  const dim3 grid((p.N + C - 1) / C), block(64 * kDirectWaves);
+  const size_t lds = (size_t)p.M * (p.Kb + 16);
+  const int steps = (p.Kb + DirectGeom<DenseI8, Q>::kStep - 1) / DirectGeom<DenseI8, Q>::kStep;
+  if (steps <= 4)
+    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 4>), grid, block, lds, stream, p, x, ld_x);
+  else
+    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 8>), grid, block, lds, stream, p, x, ld_x);
+  return hipGetLastError();
 }
 
 // The tiled kernel's variants, widest tile first: what one stage takes with at
@@ -219,12 +295,12 @@ struct Variant {
 constexpr Variant kVariants[] = {
     {256, 224, 1, 1360, 0, 10500}, {128, 224, 1, 850, 0, 3500}, {128, 128, 1, 500, 0, 3000},
     {128, 128, 2, 720, 930, 3000}, {64, 128, 2, 290, 550, 2000}, {64, 64, 2, 170, 340, 1500},
-    {32, 64, 2, 110, 225, 1500},   {32, 32, 2, 80, 123, 1500},
+    {32, 64, 2, 110, 225, 1500},   {32, 32, 2, 95, 135, 1500},
 };
 constexpr int kNumVariants = sizeof(kVariants) / sizeof(kVariants[0]);
-constexpr int kCus = 256;
 constexpr int kMaxSplits = 16;
-constexpr int kDirectRows = 16;
+constexpr int kDirectRows = 16;        // up to here always the direct kernel
+constexpr int kDirectMost = 256;       // up to here the direct kernel if it is estimated faster
 constexpr int kFusedRows = 8;          // tokens that the one-launch INT8 call quantises itself
 constexpr int kFusedBytes = 44 << 10;  // their codes in LDS, next to 16 KB of partial tiles
 
@@ -233,14 +309,14 @@ struct Pick {
   int splits;
 };
 
-// The variant and split of K with the least estimated time: whole rounds of
-// workgroups at their stage time, plus, with K split, the partial sums'
+// The kernel, variant and split of K with the least estimated time: whole rounds
+// of workgroups at their stage time, 4 us of launch, first loads and epilogue, plus, with K split, the partial sums'
 // way through memory (4 bytes/ps) and a second launch.
 Pick pick(int M, int N, int64_t Kb) {
   if (M <= kDirectRows) return {-1, 1};
   const int stages = (int)((Kb + kStageK - 1) / kStageK);
   Pick best{-1, 1};
-  float least = 0;
+  float least = M <= kDirectMost ? 2300.0f + direct_ns(direct_q(M, N, Kb), M, N, Kb) : 3.4e38f;
   for (int v = 0; v < kNumVariants; ++v) {
     const Variant& c = kVariants[v];
     const int64_t tiles = (int64_t)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
@@ -250,10 +326,10 @@ Pick pick(int M, int N, int64_t Kb) {
       const int per = (stages + s - 1) / s;
       const int64_t wgs = tiles * s, full = wgs / (kCus * c.per_cu), rest = wgs % (kCus * c.per_cu);
       const float whole = per * (c.per_cu == 2 ? c.two : c.one) + c.fixed;
-      float t = full * whole;
+      float t = 4000.0f + full * whole;
       if (rest) t += rest <= kCus ? per * c.one + c.fixed : whole;
       if (s > 1) t += 2500.0f + (float)s * M * N * 8 / 4000.0f;
-      if (best.variant < 0 || t < least) {
+      if (t < least) {
         least = t;
         best = {v, s};
       }
@@ -292,27 +368,18 @@ size_t dense_workspace(int M, int N, int64_t Kb) {
 }
 
 bool dense_fuses_quant(int M, int N, int K) {
-  return M <= kFusedRows && (int64_t)M * (K + 16) <= kFusedBytes && M <= 16 / direct_q(M, N);
+  if (M > 1 && (N + 15) / 16 > kCus) return false;
+  return M <= kFusedRows && M * ((K + 511) / 512) <= kFusedUnits * kDirectWaves &&
+         M * (K + 16) <= kFusedBytes;
 }
 
 hipError_t launch_dense_quant(const DenseParams& p, const uint16_t* x, int64_t ld_x,
                               hipStream_t stream) {
-  const size_t lds = (size_t)p.M * (p.Kb + 16);
-  const dim3 block(64 * kDirectWaves);
-  switch (direct_q(p.M, p.N)) {
-    case 1:
-      hipLaunchKernelGGL((dense_direct_quant_kernel<1>), dim3((p.N + 15) / 16), block, lds, stream,
-                         p, x, ld_x);
-      break;
-    case 2:
-      hipLaunchKernelGGL((dense_direct_quant_kernel<2>), dim3((p.N + 7) / 8), block, lds, stream,
-                         p, x, ld_x);
-      break;
-    default:
-      hipLaunchKernelGGL((dense_direct_quant_kernel<4>), dim3((p.N + 3) / 4), block, lds, stream,
-                         p, x, ld_x);
+  switch (fused_q(p.M, p.N)) {
+    case 1: return direct_quant<1>(p, x, ld_x, stream);
+    case 2: return direct_quant<2>(p, x, ld_x, stream);
+    default: return direct_quant<4>(p, x, ld_x, stream);
   }
-  return hipGetLastError();
 }
 
 hipError_t launch_dense(bool i8, const DenseParams& p, hipStream_t stream) {

@@ -238,10 +238,48 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
     }
     return;
   }
+  // A tile at an edge, or rows that take no vector stores: through LDS (each
+  // wavefront its own part, 16 rows at a time), so that a store instruction
+  // writes neighbouring elements of a row.
+  asm volatile("s_barrier" ::: "memory");   // the ring is no longer read
+  constexpr int kRow = 16 * NI + 4;         // floats; the pad spreads the rows over the banks
+  static_assert(W * 16 * kRow * 4 <= NBUF * kStage, "epilogue rows fit in the ring");
+  float* rows = reinterpret_cast<float*>(lds) + wave * 16 * kRow;
+  const int m_b = m0 + 16 * MI * wm, n_b = n0 + 16 * NI * wn;
+  for (int i = 0; i < MI; ++i) {
+    v4f f[NI];
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+    for (int ii = 0; ii < MI; ++ii)
+      if (ii == i) {
 #pragma unroll
-    for (int j = 0; j < NI; ++j) dense_store<T>(p, acc[i][j], m_w + 16 * i, n_w + 16 * j);
+        for (int j = 0; j < NI; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[j][e] = (float)acc[ii][j][e];
+      }
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+      *reinterpret_cast<v4f*>(rows + r * kRow + 16 * j + 4 * g) = f[j];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll 4
+    for (int e = lane; e < 16 * 16 * NI; e += 64) {
+      const int row = e / (16 * NI), col = e - row * 16 * NI;
+      const int m = m_b + 16 * i + row, n = n_b + col;
+      if (m < p.M && n < p.N) {
+        float v = rows[row * kRow + col];
+        if constexpr (T::kInt) v = v * p.sx[m] * p.sw[n];
+        const int64_t o = (int64_t)m * p.ld_out + n;
+        if (p.out_f32)
+          static_cast<float*>(p.out)[o] = v;
+        else
+          static_cast<uint16_t*>(p.out)[o] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
 }
 
 template <class T, int WM, int WN, int MI, int NI, int NBUF, int WPE>
