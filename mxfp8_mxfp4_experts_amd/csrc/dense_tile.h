@@ -111,7 +111,29 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
           kStageK * s, 0, 0);
   };
 
+  // The epilogue's scales: before the loop where registers allow it, so that
+  // their way from memory is not at the end.
+  const int m_w = m0 + 16 * MI * wm + r, n_w = n0 + 16 * NI * wn + 4 * g;
+  constexpr bool kEarly = MI * NI <= 16;
+  float sx[MI], sw[NI][4];
+  auto load_scales = [&]() __attribute__((always_inline)) {
+    if constexpr (T::kInt) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) sx[i] = p.sx[min(m_w + 16 * i, p.M - 1)];
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sw[j][e] = p.sw[min(n_w + 16 * j + e, p.N - 1)];
+    }
+  };
+  if constexpr (kEarly) load_scales();
+
   Acc acc[MI][NI];
+  auto value = [&](int i, int j, int e) __attribute__((always_inline)) {
+    float f = (float)acc[i][j][e];
+    if constexpr (T::kInt) f = f * sx[i] * sw[j][e];
+    return f;
+  };
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -190,7 +212,6 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the loads past the last stage
 
-  const int m_w = m0 + 16 * MI * wm + r, n_w = n0 + 16 * NI * wn + 4 * g;
   if (cut.splits > 1) {
     // Partial sums [split][M][N rounded up to 4].
     const int64_t ldp = (p.N + 3) & ~3;
@@ -204,29 +225,17 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
       }
     return;
   }
+  if constexpr (!kEarly) load_scales();
   if (m0 + BM <= p.M && n0 + BN <= p.N && p.out_vec) {
     // A whole tile: one address per row block, no checks.
-    float sx[MI];
-    if constexpr (T::kInt) {
-#pragma unroll
-      for (int i = 0; i < MI; ++i) sx[i] = p.sx[m_w + 16 * i];
-    }
     const int64_t at = (int64_t)m_w * p.ld_out + n_w;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      float sw[4];
-      if constexpr (T::kInt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sw[e] = p.sw[n_w + 16 * j + e];
-      }
+    for (int j = 0; j < NI; ++j)
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         float f[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f[e] = (float)acc[i][j][e];
-          if constexpr (T::kInt) f[e] = f[e] * sx[i] * sw[e];
-        }
+        for (int e = 0; e < 4; ++e) f[e] = value(i, j, e);
         const int64_t o = at + 16 * i * p.ld_out + 16 * j;
         if (p.out_f32)
           *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) =
@@ -235,7 +244,6 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) =
               make_uint2(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]));
       }
-    }
     return;
   }
   // A tile at an edge, or rows that take no vector stores: through LDS (each
@@ -246,6 +254,9 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
   static_assert(W * 16 * kRow * 4 <= NBUF * kStage, "epilogue rows fit in the ring");
   float* rows = reinterpret_cast<float*>(lds) + wave * 16 * kRow;
   const int m_b = m0 + 16 * MI * wm, n_b = n0 + 16 * NI * wn;
+  // A store instruction covers kRows rows (narrow tiles) or 64 columns of one.
+  constexpr int kRows = NI < 4 ? 4 / NI : 1, kColSteps = (16 * NI + 63) / 64;
+  const int row0 = NI < 4 ? lane / (16 * NI) : 0, col0 = NI < 4 ? lane % (16 * NI) : lane;
   for (int i = 0; i < MI; ++i) {
     v4f f[NI];
 #pragma unroll
@@ -254,7 +265,7 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
 #pragma unroll
         for (int j = 0; j < NI; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[j][e] = (float)acc[ii][j][e];
+          for (int e = 0; e < 4; ++e) f[j][e] = value(ii, j, e);
       }
 #pragma unroll
     for (int j = 0; j < NI; ++j)
@@ -263,17 +274,20 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll 4
-    for (int e = lane; e < 16 * 16 * NI; e += 64) {
-      const int row = e / (16 * NI), col = e - row * 16 * NI;
-      const int m = m_b + 16 * i + row, n = n_b + col;
-      if (m < p.M && n < p.N) {
-        float v = rows[row * kRow + col];
-        if constexpr (T::kInt) v = v * p.sx[m] * p.sw[n];
-        const int64_t o = (int64_t)m * p.ld_out + n;
-        if (p.out_f32)
-          static_cast<float*>(p.out)[o] = v;
-        else
-          static_cast<uint16_t*>(p.out)[o] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
+    for (int row = row0; row < 16; row += kRows) {
+      const int m = m_b + 16 * i + row;
+      if (m >= p.M) continue;
+      const int64_t o = (int64_t)m * p.ld_out + n_b;
+#pragma unroll
+      for (int c = 0; c < kColSteps; ++c) {
+        const int col = col0 + 64 * c;
+        if (col < 16 * NI && n_b + col < p.N) {
+          const float v = rows[row * kRow + col];
+          if (p.out_f32)
+            static_cast<float*>(p.out)[o + col] = v;
+          else
+            static_cast<uint16_t*>(p.out)[o + col] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
+        }
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

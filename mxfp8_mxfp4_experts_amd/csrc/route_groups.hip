@@ -17,18 +17,24 @@
 // the kernel, so the choice is narrowed in float first, with a margin that
 // covers the float evaluation's error, and only the candidates (usually 16 to
 // 40 of hundreds) get their exact scores:
-//   * float scores differ from the exact ones by less than kScoreErr = 2^-20:
-//     the exponent's argument carries |l| 2^-24 relative, which the sigmoid
-//     damps to s(1-s)|l| 2^-24 < 2^-26; v_exp_f32 and v_rcp_f32 are within an
-//     ulp (2^-23), the sum and the product round once each;
-//   * a key adds bias in float, rounding by at most 2^-24 |key| on each side;
+//   * float scores differ from the exact ones by less than kScoreErr = 2^-21.
+//     Sigmoid: the exponent's argument rounds by |l| 2^-24 relative, which is
+//     s(1-s)|l| 2^-24 < 2^-26 of the score, v_exp_f32's ulp s(1-s) 2^-23 <=
+//     2^-25, the sum and the rounding of the exact score 2^-24 and 2^-25,
+//     v_rcp_f32's ulp 2^-23: below 2^-22 together.  Softmax: two roundings of the
+//     argument x, p|x| 2^-23 < 2^-24, exponential, scale and product 2^-23 +
+//     2^-24 + 2^-24, the exact score's 2^-25: below 2^-21.5;
+//   * a key adds bias in float, rounding by at most 2^-24 |key| on each side
+//     (kKeyRel = 2^-23 for both), and so does the sum of two keys;
 //   * an expert among the K largest exact keys then has a float key above the
 //     K-th largest float key less twice that error; the K-th largest of the
 //     lanes' largest keys is a lower bound of that, found by bisection with
 //     ballots.
-// Where float cannot tell (worths of the last group in and the first one out
-// within their error, more than 64 candidates, NaN or huge keys), the
-// wavefront evaluates everything exactly instead.
+// Where the worths of the last group inside and the first one outside are
+// within their errors (about one token in 3000 at 896 experts in 8 groups), the
+// groups' worths are taken exactly, again from candidates only.  With more than
+// 64 candidates, or NaN or huge keys, the wavefront evaluates everything
+// exactly.
 #include "common.h"
 #include "launch.h"
 #include "route_dev.h"
@@ -39,9 +45,8 @@ namespace {
 
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kInf = __builtin_inff();
-constexpr float kScoreErr = 9.5367431640625e-07f;     // 2^-20
-constexpr float kKeyRel = 2.384185791015625e-07f;     // 2^-22
-constexpr uint32_t kHuge = 0xFB800000u;   // the ordered key of 2^120: sums of two stay finite
+constexpr float kScoreErr = 4.76837158203125e-07f;     // 2^-21
+constexpr float kKeyRel = 1.1920928955078125e-07f;     // 2^-23
 constexpr int kWaves = 4;
 
 // The float that ordered_key mapped to k.
@@ -56,10 +61,35 @@ __device__ __forceinline__ uint32_t route_key(float logit, float score, float bi
   return (logit <= kLowest || key == -kInf) ? 0u : ordered_key(key);
 }
 
+// Largest float of the wavefront; no NaN among them.
 __device__ __forceinline__ float wave_fmax(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-  return v;
+  return key_value(wave_max_u32(ordered_key(v)));
+}
+
+// The best two keys of two disjoint sets, (k0, k1) and another lane's.
+template <int CTRL>
+__device__ __forceinline__ void top2_dpp(uint32_t& k0, uint32_t& k1) {
+  const uint32_t o0 = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)k0, CTRL, 0xf, 0xf, false);
+  const uint32_t o1 = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)k1, CTRL, 0xf, 0xf, false);
+  k1 = umax32(umin32(k0, o0), umax32(k1, o1));
+  k0 = umax32(k0, o0);
+}
+__device__ __forceinline__ void top2_xor(uint32_t& k0, uint32_t& k1, int off) {
+  const uint32_t o0 = (uint32_t)__shfl_xor((int)k0, off);
+  const uint32_t o1 = (uint32_t)__shfl_xor((int)k1, off);
+  k1 = umax32(umin32(k0, o0), umax32(k1, o1));
+  k0 = umax32(k0, o0);
+}
+// Over each run of 1 << log2l lanes, the same result in all of them: pairs by
+// quad permutation, quads and halves of a row by mirroring (lanes already hold
+// their quad's result, so any lane of the other quad will do), rows by shuffles.
+__device__ __forceinline__ void top2_lanes(uint32_t& k0, uint32_t& k1, int log2l) {
+  if (log2l > 0) top2_dpp<0xB1>(k0, k1);    // quad_perm [1, 0, 3, 2]
+  if (log2l > 1) top2_dpp<0x4E>(k0, k1);    // quad_perm [2, 3, 0, 1]
+  if (log2l > 2) top2_dpp<0x141>(k0, k1);   // row_half_mirror
+  if (log2l > 3) top2_dpp<0x140>(k0, k1);   // row_mirror
+  if (log2l > 4) top2_xor(k0, k1, 16);
+  if (log2l > 5) top2_xor(k0, k1, 32);
 }
 __device__ __forceinline__ double wave_dsum(double v) {
 #pragma unroll
@@ -87,12 +117,18 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Set bits of mask below this lane's.
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
 struct WaveLds {
   uint32_t* keys;      // [E]: the exact path's keys
   uint64_t* cand;      // [64]
   float* score;        // [64]: candidates' scores, then the slots'
   int* id;             // [64]
-  uint32_t* worth;     // [kMaxGroups]
+  uint32_t* worth;     // [kMaxGroups], the exact path's
 };
 
 // Lane k's expert by the exact scores of all experts (-1: none).
@@ -100,6 +136,7 @@ template <bool SOFTMAX>
 __device__ int exact_choice(const RouteGroupsParams& p, const float* row, const Softmax& sm,
                             const WaveLds& s, int lane) {
   const int E = p.E, K = p.K, G = p.n_group, per = E / G;
+#pragma unroll 4
   for (int e = lane; e < E; e += 64) {
     const float l = row[e];
     s.keys[e] = route_key(l, exact_score<SOFTMAX>(l, sm), p.bias ? p.bias[e] : 0.0f);
@@ -113,13 +150,7 @@ __device__ int exact_choice(const RouteGroupsParams& p, const float* row, const 
         k1 = umax32(k1, umin32(k0, k));
         k0 = umax32(k0, k);
       }
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) {
-        const uint32_t o0 = (uint32_t)__shfl_xor((int)k0, off);
-        const uint32_t o1 = (uint32_t)__shfl_xor((int)k1, off);
-        k1 = umax32(umin32(k0, o0), umax32(k1, o1));
-        k0 = umax32(k0, o0);
-      }
+      top2_lanes(k0, k1, 6);
       uint32_t w = k0;           // 0: every expert of the group is masked
       if (p.group_score == MOE_GROUP_TOP2 && k1 != 0u)
         w = ordered_key(key_value(k0) + key_value(k1));
@@ -170,7 +201,13 @@ __device__ __forceinline__ void write_slots(const RouteGroupsParams& p, int64_t 
     s.score[lane] = sc;
     wave_lds_fence();
     double sum = 0.0;
-    for (int k = 0; k < p.K; ++k) sum += (double)s.score[k];   // left to right
+    for (int k = 0; k < p.K; k += 8) {                         // left to right
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = s.score[k + i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += k + i < p.K ? (double)v[i] : 0.0;
+    }
     w = sum == 0.0 ? 0.0 : w / sum;
   }
   if (lane < p.K) {
@@ -178,6 +215,19 @@ __device__ __forceinline__ void write_slots(const RouteGroupsParams& p, int64_t 
     p.topk_w[t * p.K + lane] = id >= 0 ? (float)(w * (double)p.scaling) : 0.0f;
   }
 }
+
+// Float keys of the narrowed choice as unsigned numbers in the same order: the
+// ordered key less that of -inf, so 0 is "may not be taken" and a negative NaN,
+// wrapping around, is the largest of all.
+constexpr uint32_t kKeyBase = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t near_key(float f) {
+  const uint32_t b = __float_as_uint(f);
+  return (b ^ ((uint32_t)((int)b >> 31) | 0x80000000u)) - kKeyBase;
+}
+__device__ __forceinline__ float near_value(uint32_t k) { return key_value(k + kKeyBase); }
+// Keys of 2^120 and above, NaN among them; keys of -2^120 and below are the
+// numbers 1 .. kLowOdd.  Sums of two keys between those stay finite.
+constexpr uint32_t kHighOdd = 0xFB800000u - kKeyBase, kLowOdd = 0x047FFFFFu - kKeyBase;
 
 // The narrowed choice.  The wavefront's 64 lanes are split evenly over the
 // groups (L lanes each, L = 64 over n_group rounded up to a power of two);
@@ -189,14 +239,22 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
                                                 const WaveLds& s, int lane) {
   const int E = p.E, K = p.K, G = p.n_group, per = E / G;
   const int L = 1 << log2l, g = lane >> log2l, i0 = lane & (L - 1);
+  const int slots = (per + L - 1) >> log2l;          // uniform, <= S
+  const int left = g < G ? per - i0 : 0;             // this lane's experts: L j < left
+  const uint32_t e0 = (uint32_t)((g < G ? g : G - 1) * per), last = (uint32_t)(per - 1);
   float l[S], b[S];
 #pragma unroll
-  for (int j = 0; j < S; ++j) {
-    const int i = i0 + L * j;
-    const bool in = g < G && i < per;
-    l[j] = in ? row[g * per + i] : -kInf;
-    b[j] = in && p.bias ? p.bias[g * per + i] : 0.0f;
+  for (int j = 0; j < S; ++j) l[j] = row[e0 + umin32((uint32_t)(i0 + L * j), last)];
+  if (p.bias) {
+#pragma unroll
+    for (int j = 0; j < S; ++j) b[j] = p.bias[e0 + umin32((uint32_t)(i0 + L * j), last)];
+  } else {
+#pragma unroll
+    for (int j = 0; j < S; ++j) b[j] = 0.0f;
   }
+#pragma unroll
+  for (int j = 0; j < S; ++j)
+    if (L * j >= left) l[j] = -kInf;
   float scale = 1.0f, top = 0.0f;
   if constexpr (SOFTMAX) {
     top = -kInf;
@@ -207,57 +265,100 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
     double part = 0.0;
 #pragma unroll
     for (int j = 0; j < S; ++j)
-      if (!(l[j] <= kLowest)) part += exp((double)l[j] - (double)top);
+      if (j < slots) part += l[j] <= kLowest ? 0.0 : exp((double)l[j] - (double)top);
     sm.top = top;
     sm.total = wave_dsum(part);
     scale = (float)(1.0 / sm.total);
   }
-  uint32_t key[S], best = 0, second = 0;
-  bool odd = false;
+  uint32_t key[S], best = 0, second = 0, low = ~0u;
 #pragma unroll
   for (int j = 0; j < S; ++j) {
+    key[j] = 0;
+    if (j >= slots) continue;
     float a;
     if constexpr (SOFTMAX)
       a = __builtin_amdgcn_exp2f((l[j] - top) * 1.44269504f) * scale;
     else
       a = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[j] * -1.44269504f));
-    key[j] = route_key(l[j], a, b[j]);
-    odd |= key[j] >= kHuge || (key[j] != 0u && key[j] <= ~kHuge);
+    key[j] = near_key(l[j] <= kLowest ? -kInf : a + b[j]);
+    low = umin32(low, key[j] - 1u);
     second = umax32(second, umin32(best, key[j]));
     best = umax32(best, key[j]);
   }
-  if (__ballot(odd)) return false;
+  if (__ballot(best >= kHighOdd || low < kLowOdd)) return false;
 
   if (G > 1) {
     uint32_t k0 = best, k1 = second;
-    for (int off = L >> 1; off > 0; off >>= 1) {
-      const uint32_t o0 = (uint32_t)__shfl_xor((int)k0, off);
-      const uint32_t o1 = (uint32_t)__shfl_xor((int)k1, off);
-      k1 = umax32(umin32(k0, o0), umax32(k1, o1));
-      k0 = umax32(k0, o0);
-    }
+    top2_lanes(k0, k1, log2l);
     // Every lane of a group now has its best two keys.
-    float w = k0 ? key_value(k0) : -kInf;
+    float w = k0 ? near_value(k0) : -kInf;
     float err = kScoreErr + kKeyRel * fabsf(k0 ? w : 0.0f);
     if (p.group_score == MOE_GROUP_TOP2 && k1) {
-      const float v = key_value(k1);
+      const float v = near_value(k1);
       err += kScoreErr + kKeyRel * fabsf(v);
       w += v;
       err += kKeyRel * fabsf(w);
     }
     int before = 0;
-    float out_top = -kInf;       // the best worth below this group's rank, with its error
     for (int j = 0; j < G; ++j) {
-      const float o = __shfl(w, j << log2l);
+      const float o =
+          __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), j << log2l));
       before += (o > w || (o == w && j < g)) ? 1 : 0;
     }
-    const bool in = g < G && before < p.topk_group;
+    bool in = g < G && before < p.topk_group;
     // Certain if every group inside stands above every one outside by their errors.
-    float lo = in && k0 ? w - err : kInf;
-    if (g < G && !in && k0) out_top = w + err;
-    lo = -wave_fmax(-lo);
-    out_top = wave_fmax(out_top);
-    if (!(lo > out_top)) return false;
+    const float lo = -wave_fmax(in && k0 ? err - w : -kInf);
+    const float out_top = wave_fmax(g < G && !in && k0 ? w + err : -kInf);
+    if (!(lo > out_top)) {
+      // Else the groups' exact worths, from the few experts that can be among
+      // their group's best.
+      uint32_t from = 1u;
+      const uint32_t kth = p.group_score == MOE_GROUP_TOP2 && k1 ? k1 : k0;
+      if (kth) {
+        const float v = near_value(kth);
+        from = umax32(1u, near_key(v - 4.0f * (kScoreErr + kKeyRel * fabsf(v))));
+      }
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        const bool c = key[j] >= from;
+        const uint64_t mask = __ballot(c);
+        const int at = n + lanes_below(mask);
+        n += __popcll(mask);
+        if (c && at < 64) s.id[at] = (int)e0 + i0 + L * j;
+      }
+      if (n > 64) return false;
+      wave_lds_fence();
+      uint64_t mine = 0;             // the exact key, and its group's number plus one
+      if (lane < n) {
+        const int id = s.id[lane];
+        const float cl = row[id];
+        mine = ((uint64_t)route_key(cl, exact_score<SOFTMAX>(cl, sm), p.bias ? p.bias[id] : 0.0f)
+                << 32) | (uint64_t)(id / per + 1);
+      }
+      s.cand[lane] = mine;
+      wave_lds_fence();
+      uint32_t x0 = 0, x1 = 0;       // lane j < G: group j's best two exact keys
+      for (int j = 0; j < n; j += 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint64_t c = s.cand[j + i];
+          const uint32_t k = (uint32_t)c == (uint32_t)lane + 1u ? (uint32_t)(c >> 32) : 0u;
+          x1 = umax32(x1, umin32(x0, k));
+          x0 = umax32(x0, k);
+        }
+      }
+      uint32_t xw = x0;
+      if (p.group_score == MOE_GROUP_TOP2 && x1) xw = ordered_key(key_value(x0) + key_value(x1));
+      before = 0;
+      for (int j = 0; j < G; ++j) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)xw, j);
+        before += (o > xw || (o == xw && j < lane)) ? 1 : 0;
+      }
+      const uint64_t keep = __ballot(lane < G && before < p.topk_group);
+      in = g < G && ((keep >> g) & 1ull);
+      wave_lds_fence();
+    }
     if (!in) {
 #pragma unroll
       for (int j = 0; j < S; ++j) key[j] = 0u;
@@ -265,42 +366,39 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
     }
   }
 
-  // A lower bound of the K-th largest key, to 20 of its bits: by the lanes'
-  // largest keys where at least K lanes hold one, else by all keys.
-  uint32_t bound = 0;
-  if (__popcll(__ballot(best != 0u)) >= K) {
-#pragma unroll 4
-    for (int bit = 31; bit >= 12; --bit) {
-      const uint32_t c = bound | (1u << bit);
-      if (__popcll(__ballot(best >= c)) >= K) bound = c;
-    }
-  } else {
-    for (int bit = 31; bit >= 12; --bit) {
-      const uint32_t c = bound | (1u << bit);
-      int n = 0;
+  // A lower bound of the K-th largest key, to its upper 16 bits (two bits a
+  // step): by the lanes' largest keys where at least K lanes hold one, else by
+  // all keys.
+  const bool by_lane = __popcll(__ballot(best != 0u)) >= K;
+  auto enough = [&](uint32_t c) __attribute__((always_inline)) {
+    if (by_lane) return __popcll(__ballot(best >= c)) >= K;
+    int n = 0;
 #pragma unroll
-      for (int j = 0; j < S; ++j) n += __popcll(__ballot(key[j] >= c));
-      if (n >= K) bound = c;
-    }
+    for (int j = 0; j < S; ++j)
+      if (j < slots) n += __popcll(__ballot(key[j] >= c));
+    return n >= K;
+  };
+  uint32_t bound = 0;
+#pragma unroll 1
+  for (int bit = 30; bit >= 16; bit -= 2) {
+    const uint32_t c1 = bound | (1u << bit), c2 = bound | (2u << bit), c3 = bound | (3u << bit);
+    const bool e1 = enough(c1), e2 = enough(c2), e3 = enough(c3);
+    bound = e3 ? c3 : e2 ? c2 : e1 ? c1 : bound;
   }
   uint32_t least = 1u;
-  if (bound > 0x00800000u) {     // below: fewer than K keys, all are candidates
-    const float v = key_value(bound);
-    least = umax32(1u, ordered_key(v - 4.0f * (kScoreErr + kKeyRel * fabsf(v))));
+  if (bound) {     // 0: fewer than K keys, all are candidates
+    const float v = near_value(bound);
+    least = umax32(1u, near_key(v - 4.0f * (kScoreErr + kKeyRel * fabsf(v))));
   }
   int n = 0;
-  const uint64_t below = (1ull << lane) - 1;
 #pragma unroll
   for (int j = 0; j < S; ++j) {
+    if (j >= slots) continue;
     const bool c = key[j] >= least;
     const uint64_t mask = __ballot(c);
-    const int at = n + __popcll(mask & below);
+    const int at = n + lanes_below(mask);
     n += __popcll(mask);
-    if (c && at < 64) {
-      s.id[at] = g * per + i0 + L * j;
-      s.score[at] = l[j];
-      s.worth[at] = __float_as_uint(b[j]);
-    }
+    if (c && at < 64) s.id[at] = (int)e0 + i0 + L * j;
   }
   if (n > 64) return false;
   wave_lds_fence();
@@ -310,15 +408,18 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
   int id = -1;
   if (lane < n) {
     id = s.id[lane];
-    const float cl = s.score[lane];
+    const float cl = row[id];
     sc = exact_score<SOFTMAX>(cl, sm);
-    const uint32_t k = route_key(cl, sc, __uint_as_float(s.worth[lane]));
+    const uint32_t k = route_key(cl, sc, p.bias ? p.bias[id] : 0.0f);
     if (k) mine = ((uint64_t)k << 32) | (uint64_t)(0xFFFFFFFFu - (uint32_t)id);
   }
   s.cand[lane] = mine;
   wave_lds_fence();
   int rank = 0;
-  for (int j = 0; j < n; ++j) rank += s.cand[j] > mine ? 1 : 0;
+  for (int j = 0; j < n; j += 8) {         // past the last: 0, above nothing
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rank += s.cand[j + i] > mine ? 1 : 0;
+  }
   // Slot k takes the candidate of rank k.
   s.id[lane] = -1;
   s.score[lane] = 0.0f;

@@ -552,6 +552,30 @@ def test_route_groups_ties_and_extremes(m, score):
 
 
 @gpu
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("group", ["top2", "max"])
+def test_route_groups_near_worths(m, score, group):
+    """Groups of equal worth (the same logits, and biases, in another order) and of worths one
+    float step apart: the choice follows the exact float values."""
+    T, E, G = 40, 512, 8
+    per = E // G
+    l, b = route_case(7, T, E), 0.1 * rand(8, E)
+    for t in range(T):
+        a, c = t % G, (t * 3 + 1) % G
+        if a == c:
+            continue
+        l[t, c * per:(c + 1) * per] = l[t, a * per:(a + 1) * per].flip(0)
+        if t % 3 == 1:     # one step up in the best expert of the copy
+            e = c * per + int(l[t, c * per:(c + 1) * per].argmax())
+            l[t, e] = torch.nextafter(l[t, e], torch.tensor(INF))
+    for g in range(1, G):
+        b[g * per:(g + 1) * per] = b[:per].flip(0) if g % 2 else b[:per]
+    for KG in (1, 3, 4, 7):
+        check_route(m, l, b, 16, G, KG, score, group, True)
+        check_route(m, l, None, 8, G, KG, score, group, False)
+
+
+@gpu
 def test_route_groups_matches_route(m):
     for T, E, K in ((7, 896, 16), (3, 2000, 16)):
         l, b = route_case(T, T, E).cuda(), 0.1 * rand(E, E).cuda()
