@@ -5,6 +5,10 @@ The layer is five C calls into ``libmi355moe.so`` (declared in
 ``MoELayer``, which issues the calls in order with one workspace (routing,
 quantisation and grouping as the one call ``moe_route_quant_permute``; with
 given top-k ids, quantisation and grouping as ``moe_quant_permute``).
+
+Around the experts there are the residual's norm with an 8-bit output, the
+router's product, group-limited routing and dense projections in 8-bit
+integers; ``MoEBlock`` runs them with a ``MoELayer`` as one MoE block.
 """
 from ._binding import (  # noqa: F401
     COMBINE_ATOMIC,
@@ -45,4 +49,5 @@ from ._binding import (  # noqa: F401
     moe_route_quant_permute,
     moe_workspace_size,
 )
+from .block import MoEBlock  # noqa: F401
 from .layer import MoELayer  # noqa: F401

@@ -111,6 +111,27 @@ class MoELayer:
             # quantisation and grouping as one call
             B.moe_quant_permute(x, idx, self.expert_offset, self.E_local, self.workspace, xq, xs,
                                 self.expert_offsets, self.sorted_route[:R], self.route_row[:R])
+        return self._experts(xq, xs, T, w, out)
+
+    def mxfp8(self, xq: torch.Tensor, xs: torch.Tensor, topk_idx: torch.Tensor,
+              topk_w: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The layer for tokens that are MXFP8 already (xq uint8 [T, H], xs
+        uint8 [T, H/32], as moe_add_rmsnorm or moe_quant_mxfp8 give them) and
+        top-k ids and weights chosen elsewhere (moe_route_groups)."""
+        T = xq.shape[0]
+        if T > self.max_tokens:
+            self._alloc(T)
+        if tuple(topk_idx.shape) != (T, self.top_k):
+            raise ValueError(f"topk_idx must be [{T}, {self.top_k}]")
+        R = T * self.top_k
+        B.moe_permute(topk_idx, self.expert_offset, self.E_local, self.workspace,
+                      self.expert_offsets, self.sorted_route[:R], self.route_row[:R])
+        return self._experts(xq, xs, T, topk_w, out)
+
+    def _experts(self, xq, xs, T, w, out):
+        """FC1 and FC2 of grouped tokens."""
+        K = self.top_k
+        R = T * K
         B.moe_fc1_situ(xq, xs, K, self.expert_offsets, self.sorted_route[:R], self.w13,
                        self.w13_s, self.workspace, self.alpha, self.beta, self.hq[:R],
                        self.hs[:R], tiled=self.tiled)
