@@ -466,12 +466,13 @@ def moe_prepack_w2(w2, w2_s):
 
 # ---------------------------------------------------------------------------
 # Around the experts.  In a decode step these kernels run for a few
-# microseconds, so what a call costs on the host counts: the checks below read
-# each property once, and the stream is taken as torch's raw handle.
+# microseconds, so what a call costs on the host counts: each property is read
+# once, and the stream and the device come as torch's raw handles.
 
 _BF16, _F32, _U8, _I8, _I32 = (torch.bfloat16, torch.float32, torch.uint8, torch.int8,
                                torch.int32)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _wrong(t, name, dtype, shape, idx):
@@ -484,39 +485,43 @@ def _wrong(t, name, dtype, shape, idx):
 def _rows(t, name, dtype, shape, idx):
     """A [T, C] tensor whose rows may be strided; returns its row stride."""
     try:
-        ok = t.dtype is dtype and t.shape == shape and t.get_device() == idx
+        if t.dtype is dtype and t.shape == shape and t.get_device() == idx:
+            if t.is_contiguous():
+                return shape[1]
+            ld, one = t.stride()
+            if one == 1 or shape[1] == 1:
+                return ld if shape[0] > 1 else shape[1]   # one row's stride says nothing
+            raise ValueError(f"{name} must have unit column stride")
     except AttributeError:
-        ok = False
-    if not ok:
-        _wrong(t, name, dtype, shape, idx)
-    ld, one = t.stride()
-    if one != 1 and shape[1] != 1:
-        raise ValueError(f"{name} must have unit column stride")
-    return ld if shape[0] > 1 else shape[1]   # the stride of a single row says nothing
+        pass
+    _wrong(t, name, dtype, shape, idx)
 
 
 def _dense(t, name, dtype, shape, idx):
     try:
-        ok = t.dtype is dtype and t.shape == shape and t.get_device() == idx
+        if t.dtype is dtype and t.shape == shape and t.get_device() == idx:
+            if t.is_contiguous():
+                return
+            raise ValueError(f"{name} must be contiguous")
     except AttributeError:
-        ok = False
-    if not ok:
-        _wrong(t, name, dtype, shape, idx)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+        pass
+    _wrong(t, name, dtype, shape, idx)
 
 
 def _begin(x, name):
     """The device index of a call whose main operand is x, which has to be the
     current device's."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+    try:
+        idx = x.get_device()
+        if idx == _current_device() and x.dim() == 2:
+            return idx
+    except (AttributeError, RuntimeError):
+        idx = -1
+    if not isinstance(x, torch.Tensor) or idx < 0:
         raise ValueError(f"{name} must be a GPU tensor")
     if x.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
-    idx = x.get_device()
-    if idx != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {x.device}, which is not the current device")
-    return idx
+    raise ValueError(f"{name} is on {x.device}, which is not the current device")
 
 
 def _new(shape, dtype, idx):
@@ -544,20 +549,20 @@ def moe_add_rmsnorm(x, weight, eps: float, residual=None, q8: int = Q8_NONE, res
     idx = _begin(x, "x")
     shape = x.shape
     T, H = shape
+    if residual is not None and residual_out is None:
+        residual_out = _new(shape, _BF16, idx)
+    if y is None and want_y:
+        y = _new(shape, _BF16, idx)
+    q_p = s_p = r_p = h_p = y_p = None
+    ld_r = ld_h = ld_y = 0
     ld_x = _rows(x, "x", _BF16, shape, idx)
     _dense(weight, "weight", _BF16, (H,), idx)
-    r_p = h_p = y_p = q_p = s_p = None
-    ld_r = ld_h = ld_y = 0
     if residual is not None:
         ld_r = _rows(residual, "residual", _BF16, shape, idx)
         r_p = residual.data_ptr()
-        if residual_out is None:
-            residual_out = _new(shape, _BF16, idx)
     if residual_out is not None:
         ld_h = _rows(residual_out, "residual_out", _BF16, shape, idx)
         h_p = residual_out.data_ptr()
-    if y is None and want_y:
-        y = _new(shape, _BF16, idx)
     if y is not None:
         ld_y = _rows(y, "y", _BF16, shape, idx)
         y_p = y.data_ptr()
@@ -572,7 +577,7 @@ def moe_add_rmsnorm(x, weight, eps: float, residual=None, q8: int = Q8_NONE, res
         q_p, s_p = xq.data_ptr(), xs.data_ptr()
     else:
         xq = xs = None
-    st = lib().moe_add_rmsnorm(x.data_ptr(), ld_x, r_p, ld_r, weight.data_ptr(), eps, T, H, q8,
+    st = (_lib or lib()).moe_add_rmsnorm(x.data_ptr(), ld_x, r_p, ld_r, weight.data_ptr(), eps, T, H, q8,
                                h_p, ld_h, y_p, ld_y, q_p, s_p, _raw_stream(idx))
     if st:
         raise MoEError("moe_add_rmsnorm", st)
@@ -590,7 +595,7 @@ def moe_quant_int8(x, xq=None, xs=None):
         xs = _new((T,), _F32, idx)
     _dense(xq, "xq", _I8, (T, H), idx)
     _dense(xs, "xs", _F32, (T,), idx)
-    st = lib().moe_quant_int8(x.data_ptr(), ld_x, T, H, xq.data_ptr(), xs.data_ptr(),
+    st = (_lib or lib()).moe_quant_int8(x.data_ptr(), ld_x, T, H, xq.data_ptr(), xs.data_ptr(),
                               _raw_stream(idx))
     if st:
         raise MoEError("moe_quant_int8", st)
@@ -633,7 +638,7 @@ def moe_int8_matmul(xq, xs, w, w_s, out=None, out_dtype=torch.bfloat16, workspac
     _dense(xs, "xs", _F32, (M,), idx)
     N = _int8_weight(w, w_s, K, idx)
     out, ld_out, kind = _int8_out(out, out_dtype, M, N, idx)
-    L = lib()
+    L = _lib or lib()
     workspace = _workspace(workspace, L.moe_int8_workspace_size, (M, N, K), idx)
     st = L.moe_int8_matmul(xq.data_ptr(), ld_xq, xs.data_ptr(), w.data_ptr(), w_s.data_ptr(), M, N,
                            K, kind, out.data_ptr(), ld_out, workspace.data_ptr(),
@@ -650,7 +655,7 @@ def moe_int8_linear(x, w, w_s, out=None, out_dtype=torch.bfloat16, workspace=Non
     ld_x = _rows(x, "x", _BF16, (M, K), idx)
     N = _int8_weight(w, w_s, K, idx)
     out, ld_out, kind = _int8_out(out, out_dtype, M, N, idx)
-    L = lib()
+    L = _lib or lib()
     workspace = _workspace(workspace, L.moe_int8_workspace_size, (M, N, K), idx)
     st = L.moe_int8_linear(x.data_ptr(), ld_x, w.data_ptr(), w_s.data_ptr(), M, N, K, kind,
                            out.data_ptr(), ld_out, workspace.data_ptr(), workspace.numel(),
@@ -677,7 +682,7 @@ def moe_gate_logits(x, w, out=None, workspace=None):
     if out is None:
         out = _new((T, E), _F32, idx)
     ld_out = _rows(out, "out", _F32, (T, E), idx)
-    L = lib()
+    L = _lib or lib()
     workspace = _workspace(workspace, L.moe_gate_workspace_size, (T, E, H), idx)
     st = L.moe_gate_logits(x.data_ptr(), ld_x, w.data_ptr(), T, E, H, out.data_ptr(), ld_out,
                            workspace.data_ptr(), workspace.numel(), _raw_stream(idx))
@@ -708,7 +713,7 @@ def moe_route_groups(logits, bias, top_k: int, n_group: int = 1, topk_group: int
         topk_w = _new(shape, _F32, idx)
     _dense(topk_idx, "topk_idx", _I32, shape, idx)
     _dense(topk_w, "topk_w", _F32, shape, idx)
-    st = lib().moe_route_groups(logits.data_ptr(), ld, b_p, T, E, top_k, n_group, topk_group,
+    st = (_lib or lib()).moe_route_groups(logits.data_ptr(), ld, b_p, T, E, top_k, n_group, topk_group,
                                 score, group_score, 1 if renormalise else 0, routed_scaling,
                                 topk_idx.data_ptr(), topk_w.data_ptr(), _raw_stream(idx))
     if st:
