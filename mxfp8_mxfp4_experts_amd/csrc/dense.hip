@@ -85,6 +85,15 @@ __device__ __forceinline__ void direct_finish(const DenseParams& p, typename T::
   }
 }
 
+// 16 bytes at k of a row of Kb bytes, zeros past its end.  The load itself is
+// unconditional (of the row's last piece there): loads under a condition would
+// make the compiler wait for all loads before any is used.
+__device__ __forceinline__ v4i load_piece(const uint8_t* row, int k, int Kb) {
+  v4i v = *reinterpret_cast<const v4i*>(row + min(k, Kb - 16));
+  if (k >= Kb) v = v4i{0, 0, 0, 0};
+  return v;
+}
+
 // kHalf steps' loads at once, twice; MORE: K is longer than that.  Short rows take
 // the small batches, whose registers let two workgroups share a CU.
 template <class T, int Q, int kHalf, bool MORE>
@@ -96,9 +105,8 @@ __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_kernel(DensePa
   const int c = (lane & 15) / Q, kq = lane % Q, g = lane >> 4;
   const int n0 = blockIdx.x * G::kCols, m0 = blockIdx.y * G::kCols;
   const int k0 = 64 * (Q * wave + kq) + 16 * g;    // K is whole 16-byte pieces
-  const uint8_t* bp = p.b + (int64_t)min(n0 + c, p.N - 1) * p.ld_b + k0;
-  const uint8_t* ap = p.a + (int64_t)min(m0 + c, p.M - 1) * p.ld_a + k0;
-  const int left = p.Kb - k0;
+  const uint8_t* bp = p.b + (int64_t)min(n0 + c, p.N - 1) * p.ld_b;
+  const uint8_t* ap = p.a + (int64_t)min(m0 + c, p.M - 1) * p.ld_a;
   Acc acc{0, 0, 0, 0};
   // With MORE the halves take turns: one's matrix instructions while the other is
   // on its way.
@@ -106,12 +114,10 @@ __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_kernel(DensePa
     v4i a[kHalf], b[kHalf];
   } one, two;
   auto load = [&](Batch& s, int k) __attribute__((always_inline)) {
-    const v4i zero{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) {
-      const int at = k + i * G::kStep;
-      s.b[i] = at < left ? *reinterpret_cast<const v4i*>(bp + at) : zero;
-      s.a[i] = at < left ? *reinterpret_cast<const v4i*>(ap + at) : zero;
+      s.b[i] = load_piece(bp, k0 + k + i * G::kStep, p.Kb);
+      s.a[i] = load_piece(ap, k0 + k + i * G::kStep, p.Kb);
     }
   };
   auto use = [&](const Batch& s) __attribute__((always_inline)) {
@@ -136,48 +142,48 @@ __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_kernel(DensePa
 
 // INT8 with bf16 tokens, in one launch: the workgroup quantises its tokens (at
 // most 16 / Q, with the rule of moe_quant_int8) into LDS while its first weight
-// loads are on their way.
-template <int Q, int kBatch>
+// loads are on their way.  kUnits: units of 512 elements per wavefront.
+template <int Q, int kBatch, int kUnits>
 __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_quant_kernel(
     DenseParams p, const uint16_t* __restrict__ x, int64_t ld_x) {
   using T = DenseI8;
   using G = DirectGeom<T, Q>;
   extern __shared__ __attribute__((aligned(16))) uint8_t tok_s[];   // [M][K + 16]
   __shared__ v4i red_s[64 * kDirectWaves];
-  __shared__ uint32_t max_s[kFusedUnits * kDirectWaves];
+  __shared__ uint32_t max_s[kUnits * kDirectWaves];
   __shared__ float sx_s[16 / Q];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = (lane & 15) / Q, kq = lane % Q, g = lane >> 4;
   const int n0 = blockIdx.x * G::kCols, K = p.Kb, M = p.M, pieces = K / 8, row_s = K + 16;
   const int units = (pieces + 63) / 64;
   const int k0 = 64 * (Q * wave + kq) + 16 * g;
-  const uint8_t* bp = p.b + (int64_t)min(n0 + c, p.N - 1) * p.ld_b + k0;
-  const int left = K - k0;
+  const uint8_t* bp = p.b + (int64_t)min(n0 + c, p.N - 1) * p.ld_b;
   const v4i zero{0, 0, 0, 0};
+  // Units of 512 elements of a token: wavefront w takes units w, w + 16, ..., all
+  // their loads at once -- before the weights', since loads come back in order --
+  // and leaves each unit's absolute maximum (as bits: a NaN counts as the
+  // largest).
+  uint4 xv[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int u = wave + kDirectWaves * i, m = u / units, q = 64 * (u - m * units) + lane;
+    // Past the last piece or token the last one again: no other maximum.
+    xv[i] = reinterpret_cast<const uint4*>(x + min(m, M - 1) * ld_x)[min(q, pieces - 1)];
+  }
+  asm volatile("" ::: "memory");
   v4i b[kBatch];
 #pragma unroll
-  for (int i = 0; i < kBatch; ++i)
-    b[i] = i * G::kStep < left ? *reinterpret_cast<const v4i*>(bp + i * G::kStep) : zero;
-
-  // Units of 512 elements of a token: wavefront w takes units w, w + 16, ..., all
-  // their loads at once, and leaves each unit's absolute maximum (as bits: a NaN
-  // counts as the largest).
-  uint4 xv[kFusedUnits];
+  for (int i = 0; i < kBatch; ++i) b[i] = load_piece(bp, k0 + i * G::kStep, K);
+  asm volatile("" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < kFusedUnits; ++i) {
-    const int u = wave + kDirectWaves * i, m = u / units, q = 64 * (u - m * units) + lane;
-    xv[i] = m < M && q < pieces ? reinterpret_cast<const uint4*>(x + m * ld_x)[q]
-                                : make_uint4(0, 0, 0, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < kFusedUnits; ++i) {
-    if (wave + kDirectWaves * i >= M * units) break;
-    const uint32_t top = wave_umax(absmax8_bits(xv[i]));
+  for (int i = 0; i < kUnits; ++i) {
+    if (wave + kDirectWaves * i >= M * units) break;   // uniform
+    const uint32_t top = wave_max_u32(absmax8_bits(xv[i]));
     if (lane == 0) max_s[wave + kDirectWaves * i] = top;
   }
-  __syncthreads();
+  lds_barrier();
 #pragma unroll
-  for (int i = 0; i < kFusedUnits; ++i) {
+  for (int i = 0; i < kUnits; ++i) {
     const int u = wave + kDirectWaves * i, m = u / units, q = 64 * (u - m * units) + lane;
     if (m >= M) break;
     uint32_t top = 0;
@@ -190,23 +196,20 @@ __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_quant_kernel(
       *reinterpret_cast<uint2*>(tok_s + m * row_s + 8 * q) = int8x8(f, s);
     }
   }
-  __syncthreads();
+  lds_barrier();
 
-  const uint8_t* ap = tok_s + min(c, M - 1) * row_s + k0;
+  const uint8_t* ap = tok_s + min(c, M - 1) * row_s;
   v4i acc = zero;
   for (int k = 0; k < K; k += kBatch * G::kStep) {
     v4i next[kBatch];
+    if (k + kBatch * G::kStep < K) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int at = k + (kBatch + i) * G::kStep;
-      next[i] = at < left ? *reinterpret_cast<const v4i*>(bp + at) : zero;
+      for (int i = 0; i < kBatch; ++i)
+        next[i] = load_piece(bp, k0 + k + (kBatch + i) * G::kStep, K);
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int at = k + i * G::kStep;
-      const v4i a = at < left ? *reinterpret_cast<const v4i*>(ap + at) : zero;
-      acc = T::mfma(b[i], a, acc);
-    }
+    for (int i = 0; i < kBatch; ++i)
+      acc = T::mfma(b[i], load_piece(ap, k0 + k + i * G::kStep, K), acc);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) b[i] = next[i];
   }
@@ -277,10 +280,17 @@ hipError_t direct_quant(const DenseParams& p, const uint16_t* x, int64_t ld_x,
   const dim3 grid((p.N + C - 1) / C), block(64 * kDirectWaves);
   const size_t lds = (size_t)p.M * (p.Kb + 16);
   const int steps = (p.Kb + DirectGeom<DenseI8, Q>::kStep - 1) / DirectGeom<DenseI8, Q>::kStep;
-  if (steps <= 4)
-    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 4>), grid, block, lds, stream, p, x, ld_x);
+  const bool one = p.M * ((p.Kb + 511) / 512) <= kDirectWaves;
+  if (steps <= 4 && one)
+    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 4, 1>), grid, block, lds, stream, p, x, ld_x);
+  else if (steps <= 4)
+    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 4, kFusedUnits>), grid, block, lds, stream, p,
+                       x, ld_x);
+  else if (one)
+    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 8, 1>), grid, block, lds, stream, p, x, ld_x);
   else
-    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 8>), grid, block, lds, stream, p, x, ld_x);
+    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 8, kFusedUnits>), grid, block, lds, stream, p,
+                       x, ld_x);
   return hipGetLastError();
 }
 
@@ -293,9 +303,9 @@ struct Variant {
   float one, two, fixed;
 };
 constexpr Variant kVariants[] = {
-    {256, 224, 1, 1360, 0, 10500}, {128, 224, 1, 850, 0, 3500}, {128, 128, 1, 500, 0, 3000},
-    {128, 128, 2, 720, 930, 3000}, {64, 128, 2, 290, 550, 2000}, {64, 64, 2, 170, 340, 1500},
-    {32, 64, 2, 110, 225, 1500},   {32, 32, 2, 95, 135, 1500},
+    {256, 224, 1, 1360, 0, 10500}, {128, 224, 1, 800, 0, 3000},   {128, 128, 1, 440, 0, 2200},
+    {128, 128, 2, 720, 900, 2500}, {64, 128, 2, 275, 540, 1500},  {64, 64, 2, 160, 320, 1200},
+    {32, 64, 2, 120, 230, 1200},   {32, 32, 2, 85, 130, 1000},
 };
 constexpr int kNumVariants = sizeof(kVariants) / sizeof(kVariants[0]);
 constexpr int kMaxSplits = 16;
@@ -311,7 +321,7 @@ struct Pick {
 
 // The kernel, variant and split of K with the least estimated time: whole rounds
 // of workgroups at their stage time, 4 us of launch, first loads and epilogue, plus, with K split, the partial sums'
-// way through memory (4 bytes/ps) and a second launch.
+// way through the caches (8 bytes/ps) and a second launch.
 Pick pick(int M, int N, int64_t Kb) {
   if (M <= kDirectRows) return {-1, 1};
   const int stages = (int)((Kb + kStageK - 1) / kStageK);
@@ -328,7 +338,7 @@ Pick pick(int M, int N, int64_t Kb) {
       const float whole = per * (c.per_cu == 2 ? c.two : c.one) + c.fixed;
       float t = 4000.0f + full * whole;
       if (rest) t += rest <= kCus ? per * c.one + c.fixed : whole;
-      if (s > 1) t += 2500.0f + (float)s * M * N * 8 / 4000.0f;
+      if (s > 1) t += 2500.0f + (float)s * M * N * 8 / 8000.0f;
       if (t < least) {
         least = t;
         best = {v, s};
@@ -349,7 +359,7 @@ hipError_t launch(const DenseParams& p, hipStream_t stream) {
   switch (k.variant) {
     case 0: return dense_tile_launch<T, 2, 2, 8, 7, 2, 1>(p, k.splits, stream);
     case 1: return dense_tile_launch<T, 2, 2, 4, 7, 3, 1>(p, k.splits, stream);
-    case 2: return dense_tile_launch<T, 2, 2, 4, 4, 4, 1>(p, k.splits, stream);
+    case 2: return dense_tile_launch<T, 4, 2, 2, 4, 4, 2>(p, k.splits, stream);
     case 3: return dense_tile_launch<T, 2, 2, 4, 4, 2, 2>(p, k.splits, stream);
     case 4: return dense_tile_launch<T, 2, 2, 2, 4, 3, 2>(p, k.splits, stream);
     case 5: return dense_tile_launch<T, 2, 2, 2, 2, 4, 2>(p, k.splits, stream);

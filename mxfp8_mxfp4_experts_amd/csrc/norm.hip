@@ -78,12 +78,12 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
   // Every wavefront adds the wavefronts' sums in the same order.
   const int wave = tid >> 6, n_waves = (int)blockDim.x >> 6;
   if constexpr (NORM) sum = wave_sum(sum);
-  if constexpr (Q8 == MOE_Q8_INT8) top = wave_umax(top);
+  if constexpr (Q8 == MOE_Q8_INT8) top = wave_max_u32(top);   // a NaN's bits are the largest: not hidden
   if ((tid & 63) == 0) {
     if constexpr (NORM) sum_s[wave] = sum;
     if constexpr (Q8 == MOE_Q8_INT8) max_s[wave] = top;
   }
-  __syncthreads();
+  lds_barrier();
   sum = 0.0f;
   top = 0;
   for (int i = 0; i < n_waves; ++i) {

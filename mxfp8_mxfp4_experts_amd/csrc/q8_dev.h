@@ -4,24 +4,34 @@
 
 #include "common.h"
 #include "fc_common.h"   // e4m3x4_scaled
+#include "route_dev.h"   // wave_max_u32
 
 namespace mi355moe {
 
+// A barrier after LDS writes that leaves global loads and stores under way (the
+// compiler's own barrier waits for them all).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  asm volatile("s_barrier" ::: "memory");
+}
+
 constexpr float kMinScale = 1.17549435e-38f;   // 2^-126: 1 / s stays finite
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+// Wavefront sum, uniform result: inclusive scans within 16-lane rows (row_shr
+// 1, 2, 4, 8), then row_bcast 15 and 31 carry the rows' sums up to lane 63.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf,
+                                                        false));
 }
-// NaN counts as the largest value: a row that holds one must not hide it.
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)v, off);
-    v = o > v ? o : v;
-  }
-  return v;
+__device__ __forceinline__ float wave_sum(float v) {
+  v = add_dpp<0x111, 0xf>(v);
+  v = add_dpp<0x112, 0xf>(v);
+  v = add_dpp<0x114, 0xf>(v);
+  v = add_dpp<0x118, 0xf>(v);
+  v = add_dpp<0x142, 0xa>(v);
+  v = add_dpp<0x143, 0xc>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
