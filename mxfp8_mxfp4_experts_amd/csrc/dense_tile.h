@@ -49,7 +49,8 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
   constexpr int kOffB = PA * W * 1024, kStage = kOffB + PB * W * 1024;
   constexpr int kLoads = PA + PB, kReads = MI + NI;
   static_assert((NBUF - 1) * kLoads < 64, "vmcnt");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NBUF * kStage];
+  constexpr int kScales = NBUF * kStage;           // then the tile's scales: BM, BN floats
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kScales + (T::kInt ? 4 * (BM + BN) : 0)];
   dense_lds_t* const lds_base = (dense_lds_t*)lds;
 
   const int lane = threadIdx.x & 63;
@@ -111,22 +112,34 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
           kStageK * s, 0, 0);
   };
 
-  // The epilogue's scales: before the loop where registers allow it, so that
-  // their way from memory is not at the end.
+  // The epilogue's scales, fetched before the loop so that their way from memory
+  // is not at the end: into registers where there is room, else into LDS (the
+  // loop's barriers lie between these writes and the epilogue's reads).
   const int m_w = m0 + 16 * MI * wm + r, n_w = n0 + 16 * NI * wn + 4 * g;
   constexpr bool kEarly = MI * NI <= 16;
+  float* const scales = reinterpret_cast<float*>(lds + kScales);
   float sx[MI], sw[NI][4];
-  auto load_scales = [&]() __attribute__((always_inline)) {
-    if constexpr (T::kInt) {
+  if constexpr (T::kInt && kEarly) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i) sx[i] = p.sx[min(m_w + 16 * i, p.M - 1)];
+    for (int i = 0; i < MI; ++i) sx[i] = p.sx[min(m_w + 16 * i, p.M - 1)];
 #pragma unroll
-      for (int j = 0; j < NI; ++j)
+    for (int j = 0; j < NI; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sw[j][e] = p.sw[min(n_w + 16 * j + e, p.N - 1)];
+      for (int e = 0; e < 4; ++e) sw[j][e] = p.sw[min(n_w + 16 * j + e, p.N - 1)];
+  }
+  if constexpr (T::kInt && !kEarly) {
+    for (int i = threadIdx.x; i < BM + BN; i += 64 * W)
+      scales[i] = i < BM ? p.sx[min(m0 + i, p.M - 1)] : p.sw[min(n0 + i - BM, p.N - 1)];
+  }
+  auto scales_of = [&](int j) __attribute__((always_inline)) {
+    if constexpr (T::kInt && !kEarly) {
+      const float4 v = *reinterpret_cast<const float4*>(scales + BM + 16 * NI * wn + 16 * j + 4 * g);
+      sw[j][0] = v.x;
+      sw[j][1] = v.y;
+      sw[j][2] = v.z;
+      sw[j][3] = v.w;
     }
   };
-  if constexpr (kEarly) load_scales();
 
   Acc acc[MI][NI];
   auto value = [&](int i, int j, int e) __attribute__((always_inline)) {
@@ -225,25 +238,60 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
       }
     return;
   }
-  if constexpr (!kEarly) load_scales();
+  if constexpr (T::kInt && !kEarly) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sx[i] = scales[16 * MI * wm + r + 16 * i];
+  }
   if (m0 + BM <= p.M && n0 + BN <= p.N && p.out_vec) {
     // A whole tile: one address per row block, no checks.
-    const int64_t at = (int64_t)m_w * p.ld_out + n_w;
+    if (p.out_f32) {
+      float* o = static_cast<float*>(p.out) + (int64_t)m_w * p.ld_out + n_w;
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
+      for (int j = 0; j < NI; ++j) {
+        scales_of(j);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        float f[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = value(i, j, e);
-        const int64_t o = at + 16 * i * p.ld_out + 16 * j;
-        if (p.out_f32)
-          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) =
-              make_float4(f[0], f[1], f[2], f[3]);
-        else
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) =
-              make_uint2(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]));
+        for (int i = 0; i < MI; ++i)
+          *reinterpret_cast<float4*>(o + 16 * i * p.ld_out + 16 * j) =
+              make_float4(value(i, j, 0), value(i, j, 1), value(i, j, 2), value(i, j, 3));
       }
+    } else {
+      uint16_t* o = static_cast<uint16_t*>(p.out) + (int64_t)m_w * p.ld_out + n_w;
+      auto pack = [&](int i, int j) __attribute__((always_inline)) {
+        return make_uint2(f32x2_to_bf16x2(value(i, j, 0), value(i, j, 1)),
+                          f32x2_to_bf16x2(value(i, j, 2), value(i, j, 3)));
+      };
+      // Two column blocks at a time: swapping the odd 16-lane rows of the first
+      // with the even rows of the second leaves every lane 8 neighbouring
+      // columns, block j in the even rows and j + 1 in the odd ones -- 64 bytes
+      // of a token's row per store instead of 32.
+      int j = 0;
+      if constexpr (NI > 1) {
+        if ((p.ld_out & 7) == 0) {
+          uint16_t* o2 = o - 4 * g + 16 * (g & 1) + 8 * (g >> 1);
+#pragma unroll
+          for (; j + 1 < NI; j += 2) {
+            scales_of(j);
+            scales_of(j + 1);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+              const uint2 u = pack(i, j), v = pack(i, j + 1);
+              const auto x = __builtin_amdgcn_permlane16_swap(u.x, v.x, false, false);
+              const auto y = __builtin_amdgcn_permlane16_swap(u.y, v.y, false, false);
+              *reinterpret_cast<uint4*>(o2 + 16 * i * p.ld_out + 16 * j) =
+                  make_uint4(x[0], y[0], x[1], y[1]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int jj = 0; jj < NI; ++jj) {
+        if (jj < j) continue;
+        scales_of(jj);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+          *reinterpret_cast<uint2*>(o + 16 * i * p.ld_out + 16 * jj) = pack(i, jj);
+      }
+    }
     return;
   }
   // A tile at an edge, or rows that take no vector stores: through LDS (each
@@ -257,6 +305,8 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
   // A store instruction covers kRows rows (narrow tiles) or 64 columns of one.
   constexpr int kRows = NI < 4 ? 4 / NI : 1, kColSteps = (16 * NI + 63) / 64;
   const int row0 = NI < 4 ? lane / (16 * NI) : 0, col0 = NI < 4 ? lane % (16 * NI) : lane;
+#pragma unroll
+  for (int j = 0; j < NI; ++j) scales_of(j);
   for (int i = 0; i < MI; ++i) {
     v4f f[NI];
 #pragma unroll
