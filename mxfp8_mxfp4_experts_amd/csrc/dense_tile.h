@@ -101,8 +101,11 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
     vb[q] = row < rows_b ? (uint32_t)(row * p.ld_b) + 16 * chunk : kPastEnd;
   }
   auto in_k = [&](int s) { return kStageK * s + 16 * chunk < k_end; };
+  // The scalar offset stays inside the buffer also past the last stage, so that
+  // what lies beyond the end is told by the lane's offset alone.
   auto issue = [&](int q, int s, int buf, bool in) __attribute__((always_inline)) {
     uint8_t* base = lds + buf * kStage;
+    s = min(s, n_all - 1);
     if (q < PA)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, base + 1024 * (PA * wave + q), 16,
                                                in ? va[q] : kPastEnd, kStageK * s, 0, 0);

@@ -124,7 +124,7 @@ __device__ __forceinline__ int lanes_below(uint64_t mask) {
 }
 
 struct WaveLds {
-  uint32_t* keys;      // [E]: the exact path's keys
+  uint32_t* keys;      // [E]: candidates' experts, or the exact path's keys
   uint64_t* cand;      // [64]
   float* score;        // [64]: candidates' scores, then the slots'
   int* id;             // [64]
@@ -197,17 +197,13 @@ __device__ __forceinline__ void write_slots(const RouteGroupsParams& p, int64_t 
                                             const WaveLds& s, int lane) {
   double w = (double)sc;
   if (p.renormalise) {
+    double* d = reinterpret_cast<double*>(s.cand);
     wave_lds_fence();
-    s.score[lane] = sc;
+    d[lane] = w;
     wave_lds_fence();
     double sum = 0.0;
-    for (int k = 0; k < p.K; k += 8) {                         // left to right
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = s.score[k + i];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum += k + i < p.K ? (double)v[i] : 0.0;
-    }
+#pragma unroll 8
+    for (int k = 0; k < p.K; ++k) sum += d[k];   // left to right
     w = sum == 0.0 ? 0.0 : w / sum;
   }
   if (lane < p.K) {
@@ -241,26 +237,31 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
   const int L = 1 << log2l, g = lane >> log2l, i0 = lane & (L - 1);
   const int slots = (per + L - 1) >> log2l;          // uniform, <= S
   const int left = g < G ? per - i0 : 0;             // this lane's experts: L j < left
-  const uint32_t e0 = (uint32_t)((g < G ? g : G - 1) * per), last = (uint32_t)(per - 1);
+  const int e0 = (g < G ? g : G - 1) * per + i0;     // its first expert
+  // Through buffers of the row's (the bias's) size: 32-bit offsets, zeros past the
+  // end and for no bias at all.
+  const __amdgpu_buffer_rsrc_t lr = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(row), 0, (uint32_t)(4 * E), 0x00020000);
+  const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(p.bias), 0, p.bias ? (uint32_t)(4 * E) : 0u, 0x00020000);
   float l[S], b[S];
 #pragma unroll
-  for (int j = 0; j < S; ++j) l[j] = row[e0 + umin32((uint32_t)(i0 + L * j), last)];
-  if (p.bias) {
-#pragma unroll
-    for (int j = 0; j < S; ++j) b[j] = p.bias[e0 + umin32((uint32_t)(i0 + L * j), last)];
-  } else {
-#pragma unroll
-    for (int j = 0; j < S; ++j) b[j] = 0.0f;
+  for (int j = 0; j < S; ++j) {
+    const int at = 4 * (e0 + L * j);   // past the row for slots that do not exist
+    l[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(lr, at, 0, 0));
+    b[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(br, at, 0, 0));
   }
+  if (per != L * slots || (G << log2l) != 64) {        // some lanes have fewer
 #pragma unroll
-  for (int j = 0; j < S; ++j)
-    if (L * j >= left) l[j] = -kInf;
+    for (int j = 0; j < S; ++j)
+      if (L * j >= left) l[j] = -kInf;
+  }
   float scale = 1.0f, top = 0.0f;
   if constexpr (SOFTMAX) {
     top = -kInf;
 #pragma unroll
     for (int j = 0; j < S; ++j)
-      if (l[j] > kLowest) top = fmaxf(top, l[j]);
+      if (j < slots && l[j] > kLowest) top = fmaxf(top, l[j]);
     top = wave_fmax(top);
     double part = 0.0;
 #pragma unroll
@@ -287,6 +288,7 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
   }
   if (__ballot(best >= kHighOdd || low < kLowOdd)) return false;
 
+  bool in = g < G;                   // whether this lane's group stays
   if (G > 1) {
     uint32_t k0 = best, k1 = second;
     top2_lanes(k0, k1, log2l);
@@ -305,7 +307,7 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
           __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), j << log2l));
       before += (o > w || (o == w && j < g)) ? 1 : 0;
     }
-    bool in = g < G && before < p.topk_group;
+    in = g < G && before < p.topk_group;
     // Certain if every group inside stands above every one outside by their errors.
     const float lo = -wave_fmax(in && k0 ? err - w : -kInf);
     const float out_top = wave_fmax(g < G && !in && k0 ? w + err : -kInf);
@@ -325,13 +327,13 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
         const uint64_t mask = __ballot(c);
         const int at = n + lanes_below(mask);
         n += __popcll(mask);
-        if (c && at < 64) s.id[at] = (int)e0 + i0 + L * j;
+        if (c) s.keys[at] = (uint32_t)(e0 + L * j);
       }
       if (n > 64) return false;
       wave_lds_fence();
       uint64_t mine = 0;             // the exact key, and its group's number plus one
       if (lane < n) {
-        const int id = s.id[lane];
+        const int id = (int)s.keys[lane];
         const float cl = row[id];
         mine = ((uint64_t)route_key(cl, exact_score<SOFTMAX>(cl, sm), p.bias ? p.bias[id] : 0.0f)
                 << 32) | (uint64_t)(id / per + 1);
@@ -359,12 +361,9 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
       in = g < G && ((keep >> g) & 1ull);
       wave_lds_fence();
     }
-    if (!in) {
-#pragma unroll
-      for (int j = 0; j < S; ++j) key[j] = 0u;
-      best = 0u;
-    }
+    if (!in) best = 0u;
   }
+  const uint64_t in_mask = __ballot(in);
 
   // A lower bound of the K-th largest key, to its upper 16 bits (two bits a
   // step): by the lanes' largest keys where at least K lanes hold one, else by
@@ -375,7 +374,7 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
     int n = 0;
 #pragma unroll
     for (int j = 0; j < S; ++j)
-      if (j < slots) n += __popcll(__ballot(key[j] >= c));
+      if (j < slots) n += __popcll(__ballot(key[j] >= c) & in_mask);
     return n >= K;
   };
   uint32_t bound = 0;
@@ -390,6 +389,7 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
     const float v = near_value(bound);
     least = umax32(1u, near_key(v - 4.0f * (kScoreErr + kKeyRel * fabsf(v))));
   }
+  if (!in) least = ~0u;              // above every key here
   int n = 0;
 #pragma unroll
   for (int j = 0; j < S; ++j) {
@@ -398,7 +398,7 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
     const uint64_t mask = __ballot(c);
     const int at = n + lanes_below(mask);
     n += __popcll(mask);
-    if (c && at < 64) s.id[at] = (int)e0 + i0 + L * j;
+    if (c) s.keys[at] = (uint32_t)(e0 + L * j);
   }
   if (n > 64) return false;
   wave_lds_fence();
@@ -407,7 +407,7 @@ __device__ __forceinline__ bool narrowed_choice(const RouteGroupsParams& p, cons
   float sc = 0.0f;
   int id = -1;
   if (lane < n) {
-    id = s.id[lane];
+    id = (int)s.keys[lane];
     const float cl = row[id];
     sc = exact_score<SOFTMAX>(cl, sm);
     const uint32_t k = route_key(cl, sc, p.bias ? p.bias[id] : 0.0f);
