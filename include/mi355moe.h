@@ -399,7 +399,8 @@ moe_status_t moe_quant_int8(const uint16_t* x, int64_t ld_x, int T, int H, int8_
                             float* xs, hipStream_t stream);
 
 /* Bytes of workspace for moe_int8_linear (and so for moe_int8_matmul) with
- * these sizes; it grows with M.  0 for invalid sizes. */
+ * these sizes; it grows with M, so a buffer for M rows serves every smaller M
+ * with the same N and K.  0 for invalid sizes. */
 size_t moe_int8_workspace_size(int M, int N, int K);
 
 /* out[m, n] = (sum_k xq[m, k] * w[n, k]) * xs[m] * w_s[n]: the sum exact in
@@ -424,8 +425,8 @@ moe_status_t moe_int8_linear(const uint16_t* x, int64_t ld_x, const int8_t* w, c
                              int M, int N, int K, int out_type, void* out, int64_t ld_out,
                              void* workspace, size_t ws_bytes, hipStream_t stream);
 
-/* Bytes of workspace for moe_gate_logits; can be 0 for valid sizes (then
- * workspace may be NULL), and is 0 for invalid ones. */
+/* Bytes of workspace for moe_gate_logits; it grows with T.  0 for T = 0 and
+ * for invalid sizes. */
 size_t moe_gate_workspace_size(int T, int E, int H);
 
 /* The router's product: logits[t, e] = sum_h x[t, h] * w[e, h], products of

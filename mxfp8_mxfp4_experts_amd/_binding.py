@@ -603,7 +603,8 @@ def moe_quant_int8(x, xq=None, xs=None):
 
 
 def moe_int8_workspace_size(M: int, N: int, K: int) -> int:
-    """Workspace bytes of moe_int8_linear and moe_int8_matmul."""
+    """Workspace bytes of moe_int8_linear and moe_int8_matmul; a buffer for M
+    rows serves fewer."""
     n = lib().moe_int8_workspace_size(M, N, K)
     if n == 0:
         raise ValueError("invalid sizes for moe_int8_workspace_size")
@@ -666,7 +667,7 @@ def moe_int8_linear(x, w, w_s, out=None, out_dtype=torch.bfloat16, workspace=Non
 
 
 def moe_gate_workspace_size(T: int, E: int, H: int) -> int:
-    """Workspace bytes of moe_gate_logits (0 where it needs none)."""
+    """Workspace bytes of moe_gate_logits; a buffer for T tokens serves fewer."""
     return lib().moe_gate_workspace_size(T, E, H)
 
 

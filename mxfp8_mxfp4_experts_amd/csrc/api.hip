@@ -76,7 +76,7 @@ struct Int8Layout {
 };
 Int8Layout int8_layout(int M, int N, int K) {
   Int8Layout l;
-  l.xq = align256(dense_workspace(M, N, K));
+  l.xq = align256(dense_workspace(M, N));
   l.xs = align256(l.xq + (size_t)M * K);
   l.total = align256(l.xs + sizeof(float) * (size_t)M + 1);
   return l;
@@ -497,7 +497,7 @@ moe_status_t moe_int8_linear(const uint16_t* x, int64_t ld_x, const int8_t* w, c
 
 size_t moe_gate_workspace_size(int T, int E, int H) {
   if (!valid_gate(T, E, H)) return 0;
-  return dense_workspace(T, E, 2 * (int64_t)H);
+  return dense_workspace(T, E);
 }
 
 moe_status_t moe_gate_logits(const uint16_t* x, int64_t ld_x, const uint16_t* w, int T, int E,
@@ -505,7 +505,7 @@ moe_status_t moe_gate_logits(const uint16_t* x, int64_t ld_x, const uint16_t* w,
                              size_t ws_bytes, hipStream_t stream) {
   if (!valid_gate(T, E, H) || ld_x < H || ld_logits < E) return MOE_ERR_SHAPE;
   if (T == 0) return MOE_OK;
-  const size_t need = dense_workspace(T, E, 2 * (int64_t)H);
+  const size_t need = dense_workspace(T, E);
   if (!x || !w || !logits || (!workspace && need > 0)) return MOE_ERR_NULL;
   if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(w, 16) || !aligned(logits, 4) ||
       !aligned(workspace, 256))

@@ -314,6 +314,14 @@ constexpr int kDirectMost = 256;       // up to here the direct kernel if it is 
 constexpr int kFusedRows = 8;          // tokens that the one-launch INT8 call quantises itself
 constexpr int kFusedBytes = 44 << 10;  // their codes in LDS, next to 16 KB of partial tiles
 
+// Most partial sums (4 bytes each) that a product of these sizes may use: grows
+// with M, so a workspace for M rows serves every smaller M.
+constexpr int64_t kMostPartials = 1 << 22;
+int64_t most_partials(int M, int N) {
+  const int64_t all = (int64_t)kMaxSplits * M * ((N + 3) / 4 * 4);
+  return all < kMostPartials ? all : kMostPartials;
+}
+
 struct Pick {
   int variant;   // -1: the direct kernel
   int splits;
@@ -332,7 +340,9 @@ Pick pick(int M, int N, int64_t Kb) {
     const int64_t tiles = (int64_t)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
     for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
       // Splits are for launches that leave CUs idle.
-      if (s > 1 && (tiles * s > 2 * kCus || stages / s < 4)) break;
+      if (s > 1 && (tiles * s > 2 * kCus || stages / s < 4 ||
+                    (int64_t)s * M * ((N + 3) / 4 * 4) > most_partials(M, N)))
+        break;
       const int per = (stages + s - 1) / s;
       const int64_t wgs = tiles * s, full = wgs / (kCus * c.per_cu), rest = wgs % (kCus * c.per_cu);
       const float whole = per * (c.per_cu == 2 ? c.two : c.one) + c.fixed;
@@ -370,12 +380,7 @@ hipError_t launch(const DenseParams& p, hipStream_t stream) {
 
 }  // namespace
 
-size_t dense_workspace(int M, int N, int64_t Kb) {
-  if (M <= 0) return 0;
-  const Pick k = pick(M, N, Kb);
-  if (k.variant < 0 || k.splits == 1) return 0;
-  return (size_t)k.splits * M * ((N + 3) / 4 * 4) * 4;
-}
+size_t dense_workspace(int M, int N) { return sizeof(float) * (size_t)most_partials(M, N); }
 
 bool dense_fuses_quant(int M, int N, int K) {
   if (M > 1 && (N + 15) / 16 > kCus) return false;

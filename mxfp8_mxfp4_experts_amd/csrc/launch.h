@@ -117,7 +117,7 @@ struct DenseParams {
   int out_vec;              // rows take 4-element vector stores
   void* partial;            // dense_workspace bytes
 };
-size_t dense_workspace(int M, int N, int64_t Kb);
+size_t dense_workspace(int M, int N);   // grows with M
 // INT8 with bf16 tokens x in one launch (p.a and p.sx unused), for the sizes
 // that dense_fuses_quant accepts; the results of launch_norm's INT8
 // quantisation and launch_dense.

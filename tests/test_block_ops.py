@@ -124,6 +124,15 @@ def test_gate_and_int8_refuse_a_small_workspace(lib):
                                    None) == NULL
 
 
+def test_workspaces_grow_with_the_rows(lib):
+    """A workspace for M rows serves every smaller M."""
+    for N, K in ((1, 64), (896, 7168), (2051, 1040), (3584, 7168)):
+        sizes = [lib.moe_int8_workspace_size(M, N, K) for M in range(0, 3000, 7)]
+        assert sizes == sorted(sizes)
+    sizes = [lib.moe_gate_workspace_size(T, 896, 7168) for T in range(0, 9000, 13)]
+    assert sizes == sorted(sizes) and sizes[0] == 0 < sizes[1]
+
+
 def test_route_groups_refusals(lib):
     def call(l=FAKE, ld=64, b=FAKE, T=4, E=64, K=4, G=4, KG=2, score=0, group=1, ren=1, idx=FAKE,
              w=FAKE):
@@ -673,6 +682,25 @@ def test_offsets_past_32_bits(m):
     l = route_case(4, 3, 64)
     wide[:, :64] = l.cuda()
     check_route(m, wide[:, :64], None, 4, 4, 2, "sigmoid", "top2", True)
+
+
+@gpu
+def test_one_workspace_for_all_batches(m):
+    """One buffer sized for the largest batch, used and left dirty by every smaller one."""
+    N, H, most = 896, 1024, 700
+    w = rand(1, N, H, scale=H ** -0.5).to(torch.bfloat16).cuda()
+    w8, s8 = m.moe_quant_int8(w)
+    x = rand(2, most, H).to(torch.bfloat16).cuda()
+    wsg = torch.full((m.moe_gate_workspace_size(most, N, H),), 0x7F, dtype=torch.uint8,
+                     device="cuda")
+    ws8 = torch.full((m.moe_int8_workspace_size(most, N, H),), 0x7F, dtype=torch.uint8,
+                     device="cuda")
+    q, s = ref.quant_int8(x.float().cpu().numpy())
+    for T in (1, 5, 16, 17, 31, 64, 100, 128, 250, 400, most):
+        check_gate(m.moe_gate_logits(x[:T], w, workspace=wsg), x[:T], w)
+        got = m.moe_int8_linear(x[:T], w8, s8, out_dtype=torch.float32, workspace=ws8)
+        want = ref.int8_matmul(q[:T], s[:T], w8.cpu().numpy(), s8.cpu().numpy())
+        assert np.array_equal(got.cpu().numpy(), want)
 
 
 @gpu
