@@ -29,19 +29,35 @@ struct DenseBf16 {
   }
 };
 
+// The scales of token m and output columns n .. n + 3 (INT8).
+struct DenseScales {
+  float x, w[4];
+};
+template <class T>
+__device__ __forceinline__ DenseScales dense_scales(const DenseParams& p, int m, int n) {
+  DenseScales s{1.0f, {1.0f, 1.0f, 1.0f, 1.0f}};
+  if constexpr (T::kInt) {
+    s.x = p.sx[min(m, p.M - 1)];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s.w[j] = p.sw[min(n + j, p.N - 1)];
+  }
+  return s;
+}
+
 // Token m's four sums for output columns n .. n + 3 (n a multiple of 4):
 // scaled (INT8: one rounding per factor, the int32 sum's conversion
 // included), rounded to the output type and stored, as one vector where the
 // row's place and the column count allow it.
 template <class T>
-__device__ __forceinline__ void dense_store(const DenseParams& p, typename T::Acc s, int m, int n) {
+__device__ __forceinline__ void dense_store(const DenseParams& p, typename T::Acc s,
+                                            const DenseScales& sc, int m, int n) {
   if (m >= p.M || n >= p.N) return;
   float f[4];
   const bool whole = n + 4 <= p.N;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     f[j] = (float)s[j];
-    if constexpr (T::kInt) f[j] = f[j] * p.sx[m] * p.sw[whole ? n + j : min(n + j, p.N - 1)];
+    if constexpr (T::kInt) f[j] = f[j] * sc.x * sc.w[j];
   }
   const int64_t at = (int64_t)m * p.ld_out + n;
   if (p.out_f32) {

@@ -55,7 +55,8 @@ __device__ __forceinline__ void direct_finish(const DenseParams& p, typename T::
       Acc s = red_s[lane];
 #pragma unroll
       for (int w = 1; w < kDirectWaves; ++w) s += red_s[64 * w + lane];
-      dense_store<T>(p, s, m0 + (lane & 15), n0 + 4 * (lane >> 4));
+      const int m = m0 + (lane & 15), n = n0 + 4 * (lane >> 4);
+      dense_store<T>(p, s, dense_scales<T>(p, m, n), m, n);
     }
   } else {
     // Entry e of a wavefront's tile: lane e / 4, element e % 4 -- row 4 (lane / 16)

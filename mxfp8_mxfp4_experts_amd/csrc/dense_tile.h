@@ -363,11 +363,13 @@ __global__ __launch_bounds__(256) void dense_join_kernel(DenseParams p, int spli
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t total = (int64_t)p.M * per_row;
   if (at >= total) return;
+  const int m = (int)(at / per_row), n = 4 * (int)(at - (int64_t)m * per_row);
+  const DenseScales sc = dense_scales<T>(p, m, n);
   const Acc* part = static_cast<const Acc*>(p.partial) + at;
   Acc s = part[0];
+#pragma unroll 4
   for (int z = 1; z < splits; ++z) s += part[z * total];
-  const int m = (int)(at / per_row);
-  dense_store<T>(p, s, m, 4 * (int)(at - (int64_t)m * per_row));
+  dense_store<T>(p, s, sc, m, n);
 }
 
 template <class T, int WM, int WN, int MI, int NI, int NBUF, int WPE>

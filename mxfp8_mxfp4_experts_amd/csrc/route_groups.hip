@@ -91,10 +91,25 @@ __device__ __forceinline__ void top2_lanes(uint32_t& k0, uint32_t& k1, int log2l
   if (log2l > 4) top2_xor(k0, k1, 16);
   if (log2l > 5) top2_xor(k0, k1, 32);
 }
+// Wavefront sum of doubles, uniform result (the steps of wave_max_u32).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dadd_dpp(double v) {
+  const long long b = __double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+  return v + __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
 __device__ __forceinline__ double wave_dsum(double v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+  v = dadd_dpp<0x111, 0xf>(v);
+  v = dadd_dpp<0x112, 0xf>(v);
+  v = dadd_dpp<0x114, 0xf>(v);
+  v = dadd_dpp<0x118, 0xf>(v);
+  v = dadd_dpp<0x142, 0xa>(v);
+  v = dadd_dpp<0x143, 0xc>(v);
+  const long long b = __double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
 
 // A token's softmax normaliser: the largest unmasked logit and the sum.
