@@ -70,21 +70,24 @@ bool valid_gate(int T, int E, int H) {
 }
 
 // Workspace of moe_int8_linear: partial sums of the product at its start,
-// then the tokens in 8 bits and their scales.
+// then the tokens in 8 bits, in rows of whole 128-byte lines, and their scales.
 struct Int8Layout {
   size_t xq, xs, total;
+  int64_t ld_q;
 };
 Int8Layout int8_layout(int M, int N, int K) {
   Int8Layout l;
   l.xq = align256(dense_workspace(M, N));
-  l.xs = align256(l.xq + (size_t)M * K);
+  l.ld_q = ((int64_t)K + 127) / 128 * 128;
+  l.xs = align256(l.xq + (size_t)M * l.ld_q);
   l.total = align256(l.xs + sizeof(float) * (size_t)M + 1);
   return l;
 }
 
-NormParams quant_params(const uint16_t* x, int64_t ld_x, int T, int H, int8_t* xq, float* xs) {
+NormParams quant_params(const uint16_t* x, int64_t ld_x, int T, int H, int8_t* xq, int64_t ld_q,
+                        float* xs) {
   return NormParams{x, ld_x, nullptr, 0, nullptr, 0.0f, T, H, nullptr, 0, nullptr, 0,
-                    reinterpret_cast<uint8_t*>(xq), reinterpret_cast<uint8_t*>(xs)};
+                    reinterpret_cast<uint8_t*>(xq), ld_q, reinterpret_cast<uint8_t*>(xs)};
 }
 
 DenseParams int8_params(const int8_t* xq, int64_t ld_xq, const float* xs, const int8_t* w,
@@ -426,7 +429,7 @@ moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ld_x, const uint16_t* re
   moe_status_t s = check_device();
   if (s != MOE_OK) return s;
   const NormParams p{x, ld_x, residual, ld_residual, weight, eps, T, H, residual_out,
-                     ld_residual_out, y, ld_y, static_cast<uint8_t*>(xq),
+                     ld_residual_out, y, ld_y, static_cast<uint8_t*>(xq), H,
                      static_cast<uint8_t*>(xs)};
   return finish(launch_norm(p, q8, true, stream));
 }
@@ -440,7 +443,7 @@ moe_status_t moe_quant_int8(const uint16_t* x, int64_t ld_x, int T, int H, int8_
     return MOE_ERR_ALIGN;
   moe_status_t s = check_device();
   if (s != MOE_OK) return s;
-  return finish(launch_norm(quant_params(x, ld_x, T, H, xq, xs), MOE_Q8_INT8, false, stream));
+  return finish(launch_norm(quant_params(x, ld_x, T, H, xq, H, xs), MOE_Q8_INT8, false, stream));
 }
 
 size_t moe_int8_workspace_size(int M, int N, int K) {
@@ -489,10 +492,11 @@ moe_status_t moe_int8_linear(const uint16_t* x, int64_t ld_x, const int8_t* w, c
     return finish(launch_dense_quant(
         int8_params(nullptr, K, nullptr, w, w_s, M, N, K, out_type, out, ld_out, workspace), x,
         ld_x, stream));
-  if (launch_norm(quant_params(x, ld_x, M, K, xq, xs), MOE_Q8_INT8, false, stream) != hipSuccess)
+  if (launch_norm(quant_params(x, ld_x, M, K, xq, l.ld_q, xs), MOE_Q8_INT8, false, stream) !=
+      hipSuccess)
     return MOE_ERR_HIP;
   return finish(launch_dense(
-      true, int8_params(xq, K, xs, w, w_s, M, N, K, out_type, out, ld_out, workspace), stream));
+      true, int8_params(xq, l.ld_q, xs, w, w_s, M, N, K, out_type, out, ld_out, workspace), stream));
 }
 
 size_t moe_gate_workspace_size(int T, int E, int H) {

@@ -86,6 +86,7 @@ struct NormParams {
   uint16_t* y;              // may be null
   int64_t ld_y;
   uint8_t* xq;
+  int64_t ld_q;
   uint8_t* xs;              // E8M0 bytes (MXFP8) or floats (INT8)
 };
 hipError_t launch_norm(const NormParams& p, int q8, bool norm, hipStream_t stream);

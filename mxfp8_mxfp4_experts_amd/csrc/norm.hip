@@ -107,12 +107,12 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
       if (p.y) reinterpret_cast<uint4*>(p.y + row * p.ld_y)[c] = pack8(f[i]);
     }
     if constexpr (Q8 == MOE_Q8_INT8) {
-      reinterpret_cast<uint2*>(p.xq + row * p.H)[c] = int8x8(f[i], s8);
+      reinterpret_cast<uint2*>(p.xq + row * p.ld_q)[c] = int8x8(f[i], s8);
     }
     if constexpr (Q8 == MOE_Q8_MXFP8) {
       uint32_t scale;
       const uint2 q = mxfp8x8(f[i], scale);
-      reinterpret_cast<uint2*>(p.xq + row * p.H)[c] = q;
+      reinterpret_cast<uint2*>(p.xq + row * p.ld_q)[c] = q;
       if ((c & 3) == 0) p.xs[row * (p.H / 32) + c / 4] = (uint8_t)scale;
     }
   }
