@@ -21,6 +21,14 @@ namespace mi355moe {
 
 namespace {
 
+// A piece of h, past the caches: what comes next reads y and the 8-bit output,
+// h only the next block.  (Stored so as well, those two made the norm of 8192 x
+// 7168 5 us faster, and the INT8 product of 256 tokens after it 4 us slower.)
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void store_past(uint16_t* row, int c, const uint4& v) {
+  __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(row) + c);
+}
+
 // One row per workgroup, P 8-element pieces per thread (piece tid + i *
 // blockDim).  NORM false: y = x (the 8-bit quantisation alone).
 template <int P, int Q8, bool NORM>
@@ -58,7 +66,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[i][j] += g[j];
       }
-      if (p.h) reinterpret_cast<uint4*>(p.h + row * p.ld_h)[c] = pack8(f[i]);
+      if (p.h) store_past(p.h + row * p.ld_h, c, pack8(f[i]));
       float g[8];
       unpack8(wv[i], g);
 #pragma unroll
@@ -137,8 +145,9 @@ hipError_t launch_p(const NormParams& p, int q8, bool norm, int threads, hipStre
 hipError_t launch_norm(const NormParams& p, int q8, bool norm, hipStream_t stream) {
   const int pieces = p.H / 8;
   // Two pieces per thread where that leaves at least two wavefronts (8192 rows of
-  // 7168: norm 100.6 us with one piece, 96.6 with two, 99.1 with four; INT8 alone
-  // 41.2, 32.3, 32.1), four for rows past 16384.
+  // 7168, before the stores went past the L2: norm 100.6 us with one piece, 96.6
+  // with two, 99.1 with four; INT8 alone 41.2, 32.3, 32.1), four for rows past
+  // 16384.
   const int per = pieces <= 64 ? 1 : pieces <= 2048 ? 2 : 4;   // H <= kMaxNormH = 32768
   const int threads = ((pieces + per - 1) / per + 63) / 64 * 64;
   if (per == 1) return launch_p<1>(p, q8, norm, threads, stream);
