@@ -466,62 +466,67 @@ def moe_prepack_w2(w2, w2_s):
 
 # ---------------------------------------------------------------------------
 # Around the experts.  In a decode step these kernels run for a few
-# microseconds, so what a call costs on the host counts: each property is read
-# once, and the stream and the device come as torch's raw handles.
+# microseconds, so what a call costs on the host counts: a compiled helper
+# (csrc_py/tensor_args.cpp) looks at each tensor once.  It only says whether a
+# tensor is plainly right; strided rows and what is wrong are found here.
 
 _BF16, _F32, _U8, _I8, _I32 = (torch.bfloat16, torch.float32, torch.uint8, torch.int8,
                                torch.int32)
 _raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+
+
+def _load_args():
+    global _head, _plain
+    try:
+        from . import _tensor_args
+    except ImportError as e:
+        raise ImportError("_tensor_args.so is missing or does not fit this torch: build it with "
+                          "`python -m mxfp8_mxfp4_experts_amd.build`") from e
+    _head, _plain = _tensor_args.head, _tensor_args.plain
+
+
+def _head(x):
+    """(device index, rows, columns) of a 2-D tensor on the current GPU, or
+    None (the helper's function takes this one's place on the first call)."""
+    _load_args()
+    return _head(x)
+
+
+def _plain(t, dtype, rows, cols, idx):
+    """The address of a contiguous tensor of this dtype, shape (``cols`` -1:
+    one-dimensional) and device, or -1 (replaced as ``_head`` is)."""
+    _load_args()
+    return _plain(t, dtype, rows, cols, idx)
+
+
+def _no_head(x, name):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    raise ValueError(f"{name} is on {x.device}, which is not the current device")
 
 
 def _wrong(t, name, dtype, shape, idx):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch.Tensor")
-    raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{idx}, got {t.dtype} "
-                     f"{tuple(t.shape)} on {t.device}")
+    if t.dtype != dtype or t.shape != shape or t.get_device() != idx:
+        raise ValueError(f"{name} must be {dtype} {shape} on cuda:{idx}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
 
 
-def _rows(t, name, dtype, shape, idx):
-    """A [T, C] tensor whose rows may be strided; returns its row stride."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == idx:
-            if t.is_contiguous():
-                return shape[1]
-            ld, one = t.stride()
-            if one == 1 or shape[1] == 1:
-                return ld if shape[0] > 1 else shape[1]   # one row's stride says nothing
-            raise ValueError(f"{name} must have unit column stride")
-    except AttributeError:
-        pass
+def _rows(t, name, dtype, T, C, idx):
+    """Address and row stride of a [T, C] tensor whose rows may be strided."""
+    _wrong(t, name, dtype, (T, C), idx)
+    ld, one = t.stride()
+    if one != 1 and C != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), ld if T > 1 else C   # one row's stride says nothing
+
+
+def _refuse(t, name, dtype, shape, idx):
     _wrong(t, name, dtype, shape, idx)
-
-
-def _dense(t, name, dtype, shape, idx):
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == idx:
-            if t.is_contiguous():
-                return
-            raise ValueError(f"{name} must be contiguous")
-    except AttributeError:
-        pass
-    _wrong(t, name, dtype, shape, idx)
-
-
-def _begin(x, name):
-    """The device index of a call whose main operand is x, which has to be the
-    current device's."""
-    try:
-        idx = x.get_device()
-        if idx == _current_device() and x.dim() == 2:
-            return idx
-    except (AttributeError, RuntimeError):
-        idx = -1
-    if not isinstance(x, torch.Tensor) or idx < 0:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if x.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
-    raise ValueError(f"{name} is on {x.device}, which is not the current device")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _new(shape, dtype, idx):
@@ -546,39 +551,51 @@ def moe_add_rmsnorm(x, weight, eps: float, residual=None, q8: int = Q8_NONE, res
     and no buffer), and for ``q8`` Q8_MXFP8 uint8 [T, H] and [T, H/32], for
     Q8_INT8 int8 [T, H] and float [T], else None.  ``residual_out`` may be
     ``x`` or ``residual`` itself."""
-    idx = _begin(x, "x")
-    shape = x.shape
-    T, H = shape
-    if residual is not None and residual_out is None:
-        residual_out = _new(shape, _BF16, idx)
-    if y is None and want_y:
-        y = _new(shape, _BF16, idx)
-    q_p = s_p = r_p = h_p = y_p = None
-    ld_r = ld_h = ld_y = 0
-    ld_x = _rows(x, "x", _BF16, shape, idx)
-    _dense(weight, "weight", _BF16, (H,), idx)
+    head = _head(x)
+    if head is None:
+        _no_head(x, "x")
+    idx, T, H = head
+    x_p, ld_x = _plain(x, _BF16, T, H, idx), H
+    if x_p < 0:
+        x_p, ld_x = _rows(x, "x", _BF16, T, H, idx)
+    w_p = _plain(weight, _BF16, H, -1, idx)
+    if w_p < 0:
+        _refuse(weight, "weight", _BF16, (H,), idx)
+    r_p = h_p = y_p = q_p = s_p = None
+    ld_r = ld_h = ld_y = H
     if residual is not None:
-        ld_r = _rows(residual, "residual", _BF16, shape, idx)
-        r_p = residual.data_ptr()
+        r_p = _plain(residual, _BF16, T, H, idx)
+        if r_p < 0:
+            r_p, ld_r = _rows(residual, "residual", _BF16, T, H, idx)
+        if residual_out is None:
+            residual_out = _new((T, H), _BF16, idx)
     if residual_out is not None:
-        ld_h = _rows(residual_out, "residual_out", _BF16, shape, idx)
-        h_p = residual_out.data_ptr()
+        h_p = _plain(residual_out, _BF16, T, H, idx)
+        if h_p < 0:
+            h_p, ld_h = _rows(residual_out, "residual_out", _BF16, T, H, idx)
+    if y is None and want_y:
+        y = _new((T, H), _BF16, idx)
     if y is not None:
-        ld_y = _rows(y, "y", _BF16, shape, idx)
-        y_p = y.data_ptr()
+        y_p = _plain(y, _BF16, T, H, idx)
+        if y_p < 0:
+            y_p, ld_y = _rows(y, "y", _BF16, T, H, idx)
     if q8 == Q8_MXFP8 or q8 == Q8_INT8:
-        kind, s_shape, s_kind = (_U8, (T, H // 32), _U8) if q8 == Q8_MXFP8 else (_I8, (T,), _F32)
+        kind, s_kind, s_cols = (_U8, _U8, H // 32) if q8 == Q8_MXFP8 else (_I8, _F32, -1)
+        s_shape = (T, s_cols) if s_cols >= 0 else (T,)
         if xq is None:
-            xq = _new(shape, kind, idx)
+            xq = _new((T, H), kind, idx)
         if xs is None:
             xs = _new(s_shape, s_kind, idx)
-        _dense(xq, "xq", kind, shape, idx)
-        _dense(xs, "xs", s_kind, s_shape, idx)
-        q_p, s_p = xq.data_ptr(), xs.data_ptr()
+        q_p = _plain(xq, kind, T, H, idx)
+        if q_p < 0:
+            _refuse(xq, "xq", kind, (T, H), idx)
+        s_p = _plain(xs, s_kind, T, s_cols, idx)
+        if s_p < 0:
+            _refuse(xs, "xs", s_kind, s_shape, idx)
     else:
         xq = xs = None
-    st = (_lib or lib()).moe_add_rmsnorm(x.data_ptr(), ld_x, r_p, ld_r, weight.data_ptr(), eps, T, H, q8,
-                               h_p, ld_h, y_p, ld_y, q_p, s_p, _raw_stream(idx))
+    st = (_lib or lib()).moe_add_rmsnorm(x_p, ld_x, r_p, ld_r, w_p, eps, T, H, q8, h_p, ld_h, y_p,
+                                         ld_y, q_p, s_p, _raw_stream(idx))
     if st:
         raise MoEError("moe_add_rmsnorm", st)
     return residual_out, y, xq, xs
@@ -586,17 +603,23 @@ def moe_add_rmsnorm(x, weight, eps: float, residual=None, q8: int = Q8_NONE, res
 
 def moe_quant_int8(x, xq=None, xs=None):
     """bf16 rows [T, H] -> int8 [T, H] and one float scale per row [T]."""
-    idx = _begin(x, "x")
-    T, H = x.shape
-    ld_x = _rows(x, "x", _BF16, (T, H), idx)
+    head = _head(x)
+    if head is None:
+        _no_head(x, "x")
+    idx, T, H = head
+    x_p, ld_x = _plain(x, _BF16, T, H, idx), H
+    if x_p < 0:
+        x_p, ld_x = _rows(x, "x", _BF16, T, H, idx)
     if xq is None:
         xq = _new((T, H), _I8, idx)
     if xs is None:
         xs = _new((T,), _F32, idx)
-    _dense(xq, "xq", _I8, (T, H), idx)
-    _dense(xs, "xs", _F32, (T,), idx)
-    st = (_lib or lib()).moe_quant_int8(x.data_ptr(), ld_x, T, H, xq.data_ptr(), xs.data_ptr(),
-                              _raw_stream(idx))
+    q_p, s_p = _plain(xq, _I8, T, H, idx), _plain(xs, _F32, T, -1, idx)
+    if q_p < 0:
+        _refuse(xq, "xq", _I8, (T, H), idx)
+    if s_p < 0:
+        _refuse(xs, "xs", _F32, (T,), idx)
+    st = (_lib or lib()).moe_quant_int8(x_p, ld_x, T, H, q_p, s_p, _raw_stream(idx))
     if st:
         raise MoEError("moe_quant_int8", st)
     return xq, xs
@@ -612,38 +635,53 @@ def moe_int8_workspace_size(M: int, N: int, K: int) -> int:
 
 
 def _int8_out(out, out_dtype, M, N, idx):
+    """The output tensor, its address, row stride and moe_out_t value."""
     if out is None:
         if out_dtype not in _OUT_TYPE:
             raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
         out = _new((M, N), out_dtype, idx)
-    elif out.dtype not in _OUT_TYPE:
-        raise ValueError(f"out must be bfloat16 or float32, got {out.dtype}")
-    return out, _rows(out, "out", out.dtype, (M, N), idx), _OUT_TYPE[out.dtype]
+    kind = out.dtype
+    if kind not in _OUT_TYPE:
+        raise ValueError(f"out must be bfloat16 or float32, got {kind}")
+    o_p, ld_out = _plain(out, kind, M, N, idx), N
+    if o_p < 0:
+        o_p, ld_out = _rows(out, "out", kind, M, N, idx)
+    return out, o_p, ld_out, _OUT_TYPE[kind]
 
 
 def _int8_weight(w, w_s, K, idx):
-    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[1] != K:
-        raise ValueError(f"w must be [N, {K}]")
-    N = w.shape[0]
-    _dense(w, "w", _I8, (N, K), idx)
-    _dense(w_s, "w_s", _F32, (N,), idx)
-    return N
+    """N and the addresses of an int8 weight [N, K] and its scales."""
+    N = w.shape[0] if isinstance(w, torch.Tensor) and w.dim() == 2 else -1
+    w_p = _plain(w, _I8, N, K, idx)
+    if w_p < 0:
+        if N < 0 or w.shape[1] != K:
+            raise ValueError(f"w must be [N, {K}]")
+        _refuse(w, "w", _I8, (N, K), idx)
+    s_p = _plain(w_s, _F32, N, -1, idx)
+    if s_p < 0:
+        _refuse(w_s, "w_s", _F32, (N,), idx)
+    return N, w_p, s_p
 
 
 def moe_int8_matmul(xq, xs, w, w_s, out=None, out_dtype=torch.bfloat16, workspace=None):
     """out [M, N] = (xq [M, K] . w [N, K]) * xs [M] * w_s [N], the sum exact in
     int32; ``out`` or ``out_dtype`` says bf16 or float32."""
-    idx = _begin(xq, "xq")
-    M, K = xq.shape
-    ld_xq = _rows(xq, "xq", _I8, (M, K), idx)
-    _dense(xs, "xs", _F32, (M,), idx)
-    N = _int8_weight(w, w_s, K, idx)
-    out, ld_out, kind = _int8_out(out, out_dtype, M, N, idx)
+    head = _head(xq)
+    if head is None:
+        _no_head(xq, "xq")
+    idx, M, K = head
+    q_p, ld_xq = _plain(xq, _I8, M, K, idx), K
+    if q_p < 0:
+        q_p, ld_xq = _rows(xq, "xq", _I8, M, K, idx)
+    x_p = _plain(xs, _F32, M, -1, idx)
+    if x_p < 0:
+        _refuse(xs, "xs", _F32, (M,), idx)
+    N, w_p, s_p = _int8_weight(w, w_s, K, idx)
+    out, o_p, ld_out, kind = _int8_out(out, out_dtype, M, N, idx)
     L = _lib or lib()
     workspace = _workspace(workspace, L.moe_int8_workspace_size, (M, N, K), idx)
-    st = L.moe_int8_matmul(xq.data_ptr(), ld_xq, xs.data_ptr(), w.data_ptr(), w_s.data_ptr(), M, N,
-                           K, kind, out.data_ptr(), ld_out, workspace.data_ptr(),
-                           workspace.numel(), _raw_stream(idx))
+    st = L.moe_int8_matmul(q_p, ld_xq, x_p, w_p, s_p, M, N, K, kind, o_p, ld_out,
+                           workspace.data_ptr(), workspace.numel(), _raw_stream(idx))
     if st:
         raise MoEError("moe_int8_matmul", st)
     return out
@@ -651,16 +689,19 @@ def moe_int8_matmul(xq, xs, w, w_s, out=None, out_dtype=torch.bfloat16, workspac
 
 def moe_int8_linear(x, w, w_s, out=None, out_dtype=torch.bfloat16, workspace=None):
     """moe_quant_int8 of x [M, K] (bf16) and moe_int8_matmul as one call."""
-    idx = _begin(x, "x")
-    M, K = x.shape
-    ld_x = _rows(x, "x", _BF16, (M, K), idx)
-    N = _int8_weight(w, w_s, K, idx)
-    out, ld_out, kind = _int8_out(out, out_dtype, M, N, idx)
+    head = _head(x)
+    if head is None:
+        _no_head(x, "x")
+    idx, M, K = head
+    x_p, ld_x = _plain(x, _BF16, M, K, idx), K
+    if x_p < 0:
+        x_p, ld_x = _rows(x, "x", _BF16, M, K, idx)
+    N, w_p, s_p = _int8_weight(w, w_s, K, idx)
+    out, o_p, ld_out, kind = _int8_out(out, out_dtype, M, N, idx)
     L = _lib or lib()
     workspace = _workspace(workspace, L.moe_int8_workspace_size, (M, N, K), idx)
-    st = L.moe_int8_linear(x.data_ptr(), ld_x, w.data_ptr(), w_s.data_ptr(), M, N, K, kind,
-                           out.data_ptr(), ld_out, workspace.data_ptr(), workspace.numel(),
-                           _raw_stream(idx))
+    st = L.moe_int8_linear(x_p, ld_x, w_p, s_p, M, N, K, kind, o_p, ld_out, workspace.data_ptr(),
+                           workspace.numel(), _raw_stream(idx))
     if st:
         raise MoEError("moe_int8_linear", st)
     return out
@@ -673,20 +714,28 @@ def moe_gate_workspace_size(T: int, E: int, H: int) -> int:
 
 def moe_gate_logits(x, w, out=None, workspace=None):
     """Router logits float [T, E] of x [T, H] and w [E, H], both bf16."""
-    idx = _begin(x, "x")
-    T, H = x.shape
-    ld_x = _rows(x, "x", _BF16, (T, H), idx)
-    if not isinstance(w, torch.Tensor) or w.dim() != 2:
-        raise ValueError(f"w must be [E, {H}]")
-    E = w.shape[0]
-    _dense(w, "w", _BF16, (E, H), idx)
+    head = _head(x)
+    if head is None:
+        _no_head(x, "x")
+    idx, T, H = head
+    x_p, ld_x = _plain(x, _BF16, T, H, idx), H
+    if x_p < 0:
+        x_p, ld_x = _rows(x, "x", _BF16, T, H, idx)
+    E = w.shape[0] if isinstance(w, torch.Tensor) and w.dim() == 2 else -1
+    w_p = _plain(w, _BF16, E, H, idx)
+    if w_p < 0:
+        if E < 0:
+            raise ValueError(f"w must be [E, {H}]")
+        _refuse(w, "w", _BF16, (E, H), idx)
     if out is None:
         out = _new((T, E), _F32, idx)
-    ld_out = _rows(out, "out", _F32, (T, E), idx)
+    o_p, ld_out = _plain(out, _F32, T, E, idx), E
+    if o_p < 0:
+        o_p, ld_out = _rows(out, "out", _F32, T, E, idx)
     L = _lib or lib()
     workspace = _workspace(workspace, L.moe_gate_workspace_size, (T, E, H), idx)
-    st = L.moe_gate_logits(x.data_ptr(), ld_x, w.data_ptr(), T, E, H, out.data_ptr(), ld_out,
-                           workspace.data_ptr(), workspace.numel(), _raw_stream(idx))
+    st = L.moe_gate_logits(x_p, ld_x, w_p, T, E, H, o_p, ld_out, workspace.data_ptr(),
+                           workspace.numel(), _raw_stream(idx))
     if st:
         raise MoEError("moe_gate_logits", st)
     return out
@@ -700,23 +749,30 @@ def moe_route_groups(logits, bias, top_k: int, n_group: int = 1, topk_group: int
     weights float [T, top_k]; -1 with weight 0 where no unmasked expert is
     left.  ``score``: SCORE_SIGMOID or SCORE_SOFTMAX; ``group_score``:
     GROUP_MAX or GROUP_TOP2."""
-    idx = _begin(logits, "logits")
-    T, E = logits.shape
-    ld = _rows(logits, "logits", _F32, (T, E), idx)
+    head = _head(logits)
+    if head is None:
+        _no_head(logits, "logits")
+    idx, T, E = head
+    l_p, ld = _plain(logits, _F32, T, E, idx), E
+    if l_p < 0:
+        l_p, ld = _rows(logits, "logits", _F32, T, E, idx)
     b_p = None
     if bias is not None:
-        _dense(bias, "bias", _F32, (E,), idx)
-        b_p = bias.data_ptr()
-    shape = (T, top_k)
+        b_p = _plain(bias, _F32, E, -1, idx)
+        if b_p < 0:
+            _refuse(bias, "bias", _F32, (E,), idx)
     if topk_idx is None:
-        topk_idx = _new(shape, _I32, idx)
+        topk_idx = _new((T, top_k), _I32, idx)
     if topk_w is None:
-        topk_w = _new(shape, _F32, idx)
-    _dense(topk_idx, "topk_idx", _I32, shape, idx)
-    _dense(topk_w, "topk_w", _F32, shape, idx)
-    st = (_lib or lib()).moe_route_groups(logits.data_ptr(), ld, b_p, T, E, top_k, n_group, topk_group,
-                                score, group_score, 1 if renormalise else 0, routed_scaling,
-                                topk_idx.data_ptr(), topk_w.data_ptr(), _raw_stream(idx))
+        topk_w = _new((T, top_k), _F32, idx)
+    i_p, w_p = _plain(topk_idx, _I32, T, top_k, idx), _plain(topk_w, _F32, T, top_k, idx)
+    if i_p < 0:
+        _refuse(topk_idx, "topk_idx", _I32, (T, top_k), idx)
+    if w_p < 0:
+        _refuse(topk_w, "topk_w", _F32, (T, top_k), idx)
+    st = (_lib or lib()).moe_route_groups(l_p, ld, b_p, T, E, top_k, n_group, topk_group, score,
+                                          group_score, 1 if renormalise else 0, routed_scaling,
+                                          i_p, w_p, _raw_stream(idx))
     if st:
         raise MoEError("moe_route_groups", st)
     return topk_idx, topk_w

@@ -2,7 +2,8 @@
 
 Run ``python -m mxfp8_mxfp4_experts_amd.build`` or call ``build()``.  Every
 source is compiled on each call (a cross-compile: no GPU is needed).
-``build_rates()`` builds the benchmark's rate probes
+``build_args()`` builds the binding's argument checks (``_tensor_args.so``),
+``build_rates()`` the benchmark's rate probes
 (``measure/libmi355rates.so``) and ``build_probes()`` the test-only probe
 library (``tests/probe/libnumprobe.so``); neither is part of the layer.
 """
@@ -80,6 +81,33 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
     return _build_so(sorted(glob.glob(os.path.join(CSRC, "*.hip"))), OUT, "lib", verbose, jobs)
 
 
+ARGS_SRC = os.path.join(PKG, "csrc_py", "tensor_args.cpp")
+ARGS_OUT = os.path.join(PKG, "_tensor_args.so")
+
+
+def build_args(verbose: bool = False) -> str:
+    """The binding's argument checks ``_tensor_args.so`` (host code against
+    torch's headers)."""
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = ARGS_OUT + ".tmp"
+    rc, out = _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    "-I", sysconfig.get_paths()["include"], "-isystem", inc, "-isystem",
+                    os.path.join(inc, "torch", "csrc", "api", "include"), ARGS_SRC, "-L", libs,
+                    "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp])
+    if rc != 0 or (out.strip() and verbose):
+        print(f"[build] tensor_args.cpp:\n{out}", file=sys.stderr)
+    if rc != 0:
+        raise RuntimeError("g++ failed; see messages above")
+    os.replace(tmp, ARGS_OUT)
+    return ARGS_OUT
+
+
 MEASURE_DIR = os.path.join(PKG, "measure")
 MEASURE_OUT = os.path.join(MEASURE_DIR, "libmi355rates.so")
 
@@ -103,5 +131,6 @@ def build_probes(verbose: bool = False) -> str:
 
 if __name__ == "__main__":
     build(verbose=True)
+    build_args(verbose=True)
     build_rates(verbose=True)
     build_probes(verbose=True)

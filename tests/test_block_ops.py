@@ -164,7 +164,56 @@ def test_binding_refuses_cpu_tensors():
 # ---------------------------------------------------------------------------
 # GPU parity.
 
+def test_tensor_checks_answer_without_throwing(lib):
+    """The compiled checks say no to what is not a plain GPU tensor, and no
+    exception passes through them."""
+    from mxfp8_mxfp4_experts_amd import _tensor_args as ck
+    bf = torch.bfloat16
+    odd = [torch.zeros(2, 4, dtype=bf), torch.zeros(2, 4, dtype=bf).to_sparse(), torch.zeros(()),
+           torch.zeros(2, 4, dtype=bf, device="meta"), None, 3, [1.0]]
+    for t in odd:
+        assert ck.head(t) is None and ck.plain(t, bf, 2, 4, 0) == -1, type(t)
+    for args in ((odd[0], bf, 2, 4), (odd[0], "bf16", 2, 4, 0), (odd[0], bf, 2.5, 4, 0)):
+        with pytest.raises(TypeError):
+            ck.plain(*args)
+
+
 gpu = pytest.mark.gpu
+
+
+@gpu
+def test_binding_refusals():
+    """What the compiled checks refuse is named by the binding."""
+    import mxfp8_mxfp4_experts_amd as m
+    e = dict(device="cuda")
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, **e)
+    w = torch.ones(64, dtype=torch.bfloat16, **e)
+    q, s = torch.zeros(4, 64, dtype=torch.int8, **e), torch.zeros(4, **e)
+    w8, s8 = torch.zeros(32, 64, dtype=torch.int8, **e), torch.ones(32, **e)
+    logits = torch.zeros(4, 16, **e)
+    for call in (
+            lambda: m.moe_add_rmsnorm(x.cpu(), w, 1e-6), lambda: m.moe_add_rmsnorm(x[0], w, 1e-6),
+            lambda: m.moe_add_rmsnorm(x.float(), w, 1e-6),
+            lambda: m.moe_add_rmsnorm(x, w[:-1], 1e-6),
+            lambda: m.moe_add_rmsnorm(x, w.repeat(2)[::2], 1e-6),
+            lambda: m.moe_add_rmsnorm(x, w, 1e-6, residual=x[:3]),
+            lambda: m.moe_add_rmsnorm(x, w, 1e-6, y=x.t().contiguous().t()),
+            lambda: m.moe_add_rmsnorm(x, w, 1e-6, q8=m.Q8_INT8, xq=q.view(torch.uint8)),
+            lambda: m.moe_add_rmsnorm(x, w, 1e-6, q8=m.Q8_MXFP8, xs=s),
+            lambda: m.moe_quant_int8(x, xs=s[:3]), lambda: m.moe_quant_int8(x.to_sparse()),
+            lambda: m.moe_int8_matmul(q, s, w8[:, :32], s8),
+            lambda: m.moe_int8_matmul(q, s, w8, s8.cpu()),
+            lambda: m.moe_int8_matmul(q, s.double(), w8, s8),
+            lambda: m.moe_int8_linear(x, w8, s8, out=torch.zeros(4, 31, **e)),
+            lambda: m.moe_int8_linear(x, w8, s8, out_dtype=torch.float16),
+            lambda: m.moe_int8_linear(x, w8, s8, workspace=s),
+            lambda: m.moe_gate_logits(x, w), lambda: m.moe_gate_logits(x, x[:, :32]),
+            lambda: m.moe_gate_logits(x, x, out=torch.zeros(4, 4, dtype=torch.bfloat16, **e)),
+            lambda: m.moe_route_groups(logits, s, 2),
+            lambda: m.moe_route_groups(logits, None, 2, topk_w=torch.zeros(4, 3, **e)),
+            lambda: m.moe_route_groups(logits.half(), None, 2)):
+        with pytest.raises((ValueError, RuntimeError)):
+            call()
 
 
 @pytest.fixture(scope="module")
