@@ -58,22 +58,26 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
   const int wm = wave % WM, wn = wave / WM;
   const int r = lane & 15, g = lane >> 4;
 
-  // Tile of this workgroup.  Workgroups go to the 8 XCDs in turn; each XCD
-  // takes a contiguous range of tiles, in blocks of up to 8 tile rows walked
-  // column by column, so the tiles in flight on one XCD share rows of A and B
-  // in its L2.
+  // Tile and split of this workgroup.  Workgroups go to the 8 XCDs in turn; each
+  // XCD takes a contiguous range of them, split by split, a split's tiles in
+  // blocks of up to 8 tile rows walked column by column, so what is in flight on
+  // one XCD shares a range of K and rows of A and B in its L2.
   const int n_tiles = cut.tiles_m * cut.tiles_n;
-  int tile;
+  int tile, split = 0;
   {
-    const int b = blockIdx.x, x = b & 7, q = n_tiles >> 3, rest = n_tiles & 7;
+    const int n = n_tiles * cut.splits, b = blockIdx.x, x = b & 7, q = n >> 3, rest = n & 7;
     tile = x * q + min(x, rest) + (b >> 3);
+    if (cut.splits > 1) {
+      split = tile / n_tiles;
+      tile -= split * n_tiles;
+    }
   }
   const int blk = tile / (8 * cut.tiles_n);
   const int rows_in = min(8, cut.tiles_m - 8 * blk);
   const int in_blk = tile - blk * 8 * cut.tiles_n;
   const int tn = in_blk / rows_in, tm = 8 * blk + in_blk - tn * rows_in;
   const int m0 = tm * BM, n0 = tn * BN;
-  const int s0 = blockIdx.y * cut.stages_per_split;
+  const int s0 = split * cut.stages_per_split;
   const int n_all = (p.Kb + kStageK - 1) / kStageK;
   const int s1 = min(n_all, s0 + cut.stages_per_split);
   const int k_end = min(p.Kb, s1 * kStageK);
@@ -231,7 +235,7 @@ __device__ __forceinline__ void dense_tile_body(const DenseParams& p, const Dens
   if (cut.splits > 1) {
     // Partial sums [split][M][N rounded up to 4].
     const int64_t ldp = (p.N + 3) & ~3;
-    Acc* part = static_cast<Acc*>(p.partial) + (int64_t)blockIdx.y * p.M * (ldp / 4);
+    Acc* part = static_cast<Acc*>(p.partial) + (int64_t)split * p.M * (ldp / 4);
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -382,7 +386,7 @@ hipError_t dense_tile_launch(const DenseParams& p, int splits, hipStream_t strea
   cut.stages_per_split = (n_all + splits - 1) / splits;
   cut.splits = (n_all + cut.stages_per_split - 1) / cut.stages_per_split;
   hipLaunchKernelGGL((dense_tile_kernel<T, WM, WN, MI, NI, NBUF, WPE>),
-                     dim3(cut.tiles_m * cut.tiles_n, cut.splits), dim3(64 * WM * WN), 0, stream,
+                     dim3(cut.tiles_m * cut.tiles_n * cut.splits), dim3(64 * WM * WN), 0, stream,
                      p, cut);
   if (cut.splits > 1) {
     const int64_t pieces = (int64_t)p.M * ((p.N + 3) / 4);
