@@ -218,21 +218,22 @@ __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_quant_kernel(
   direct_finish<T, Q>(p, acc, 0, n0, red_s);
 }
 
-// Estimated time of the direct kernel, in ns: a workgroup reads its columns and
-// its tokens, a CU about 64 bytes/ns where a load instruction takes whole 128-byte
-// lines (Q of 2 or 4) and 37 where it takes half lines, the chip its weights at
-// about 5600 bytes/ns; the first loads and the join take about 2 us at least.
-// (Router product of 32 tokens, 896 x 7168: 14.9 us with Q = 1, 9.5 with 2; INT8
-// 16 x 3584 x 7168: 8.7 us with 1, 11.2 with 2.)
+// Estimated time of the direct kernel past its launch, in ns.  A workgroup reads
+// its columns and its tokens, a CU about 90 bytes/ns where a load instruction
+// takes whole 128-byte lines (Q of 2 or 4) and 51 where it takes half lines; first
+// loads and the join take half a microsecond, longer with more sums per output;
+// the chip reads its weights at about 5600 bytes/ns.  (Router product of 32
+// tokens, 896 x 7168: 14.9 us with Q = 1, 9.5 with 2; INT8 16 x 3584 x 7168: 8.7 us
+// with 1, 11.2 with 2.)
 constexpr int kCus = 256;
 float direct_ns(int q, int M, int N, int64_t Kb) {
   const int c = 16 / q;
   const int64_t wgs = (int64_t)((N + c - 1) / c) * ((M + c - 1) / c);
-  const float per_cu = (float)((wgs + kCus - 1) / kCus) * (c + (M < c ? M : c)) * Kb /
-                       (q == 1 ? 37.0f : 64.0f);
+  const float bytes = (float)(c + (M < c ? M : c)) * Kb;
+  const float one = q == 1 ? bytes / 51.0f + 530.0f : bytes / 90.0f + (q == 2 ? 490.0f : 850.0f);
+  const float per_cu = (float)((wgs + kCus - 1) / kCus) * one;
   const float chip = (float)N * Kb / 5600.0f;
-  const float t = per_cu > chip ? per_cu : chip;
-  return t > 2000.0f ? t : 2000.0f;
+  return per_cu > chip ? per_cu : chip;
 }
 // The Q of least estimated time.
 int direct_q(int M, int N, int64_t Kb) {
@@ -297,21 +298,26 @@ hipError_t direct_quant(const DenseParams& p, const uint16_t* x, int64_t ld_x,
 
 // The tiled kernel's variants, widest tile first: what one stage takes with at
 // most one workgroup per CU and with two, and what a workgroup takes besides
-// (first loads, epilogue), in ns on 256 CUs; fitted to sweeps over M = 32 ..
-// 8192 at K = 7168 (INT8, N = 3584) and H = 7168 (BF16, N = 896).
+// (first loads, epilogue), in ns on 256 CUs.  These and the other times of the
+// estimate are fitted to every variant and split of 618 products of both types (M
+// 17 .. 8192, N 8 .. 3584, K bytes 128 .. 14336, log-uniform): what `pick` takes
+// is 1.3% slower than the best of them in the mean, 27% at worst.  64 x 64 tiles
+// come with eight wavefronts, which take short K and two workgroups per CU 1 to 4%
+// faster, and with four, which take long K in one round faster (INT8 256 x 3584 x
+// 7168: 14.0 against 14.7 us).
 struct Variant {
   int bm, bn, per_cu;
   float one, two, fixed;
 };
 constexpr Variant kVariants[] = {
-    {256, 224, 1, 1360, 0, 10500}, {128, 224, 1, 800, 0, 3000},   {128, 128, 1, 440, 0, 2200},
-    {128, 128, 2, 720, 900, 2500}, {64, 128, 2, 275, 540, 1500},  {64, 64, 2, 160, 320, 1200},
-    {32, 64, 2, 120, 230, 1200},   {32, 32, 2, 85, 130, 1000},
+    {256, 224, 1, 1400, 0, 11000}, {128, 224, 1, 760, 0, 3300}, {128, 128, 1, 440, 0, 2100},
+    {64, 128, 2, 270, 560, 1500},  {96, 64, 2, 210, 470, 1700}, {64, 64, 2, 170, 310, 1100},
+    {64, 64, 2, 165, 320, 1220},   {32, 64, 2, 100, 230, 1100}, {32, 32, 2, 85, 170, 1000},
 };
 constexpr int kNumVariants = sizeof(kVariants) / sizeof(kVariants[0]);
 constexpr int kMaxSplits = 16;
 constexpr int kDirectRows = 16;        // up to here always the direct kernel
-constexpr int kDirectMost = 256;       // up to here the direct kernel if it is estimated faster
+constexpr int kDirectMost = 512;       // up to here the direct kernel if it is estimated faster
 constexpr int kFusedRows = 8;          // tokens that the one-launch INT8 call quantises itself
 constexpr int kFusedBytes = 44 << 10;  // their codes in LDS, next to 16 KB of partial tiles
 
@@ -329,13 +335,13 @@ struct Pick {
 };
 
 // The kernel, variant and split of K with the least estimated time: whole rounds
-// of workgroups at their stage time, 4 us of launch, first loads and epilogue, plus, with K split, the partial sums'
-// way through the caches (8 bytes/ps) and a second launch.
+// of workgroups at their stage time, 2 us of launch, plus, with K split, a second
+// launch and the partial sums' way through the caches (11 bytes/ps).
 Pick pick(int M, int N, int64_t Kb) {
   if (M <= kDirectRows) return {-1, 1};
   const int stages = (int)((Kb + kStageK - 1) / kStageK);
   Pick best{-1, 1};
-  float least = M <= kDirectMost ? 2300.0f + direct_ns(direct_q(M, N, Kb), M, N, Kb) : 3.4e38f;
+  float least = M <= kDirectMost ? 1900.0f + direct_ns(direct_q(M, N, Kb), M, N, Kb) : 3.4e38f;
   for (int v = 0; v < kNumVariants; ++v) {
     const Variant& c = kVariants[v];
     const int64_t tiles = (int64_t)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
@@ -347,9 +353,9 @@ Pick pick(int M, int N, int64_t Kb) {
       const int per = (stages + s - 1) / s;
       const int64_t wgs = tiles * s, full = wgs / (kCus * c.per_cu), rest = wgs % (kCus * c.per_cu);
       const float whole = per * (c.per_cu == 2 ? c.two : c.one) + c.fixed;
-      float t = 4000.0f + full * whole;
+      float t = 2000.0f + full * whole;
       if (rest) t += rest <= kCus ? per * c.one + c.fixed : whole;
-      if (s > 1) t += 2500.0f + (float)s * M * N * 8 / 8000.0f;
+      if (s > 1) t += 1700.0f + (float)s * M * N * 8 / 11000.0f;
       if (t < least) {
         least = t;
         best = {v, s};
@@ -371,10 +377,11 @@ hipError_t launch(const DenseParams& p, hipStream_t stream) {
     case 0: return dense_tile_launch<T, 2, 2, 8, 7, 2, 1>(p, k.splits, stream);
     case 1: return dense_tile_launch<T, 2, 2, 4, 7, 3, 1>(p, k.splits, stream);
     case 2: return dense_tile_launch<T, 4, 2, 2, 4, 4, 2>(p, k.splits, stream);
-    case 3: return dense_tile_launch<T, 2, 2, 4, 4, 2, 2>(p, k.splits, stream);
-    case 4: return dense_tile_launch<T, 2, 2, 2, 4, 3, 2>(p, k.splits, stream);
-    case 5: return dense_tile_launch<T, 2, 2, 2, 2, 4, 2>(p, k.splits, stream);
-    case 6: return dense_tile_launch<T, 2, 2, 1, 2, 6, 2>(p, k.splits, stream);
+    case 3: return dense_tile_launch<T, 2, 2, 2, 4, 3, 2>(p, k.splits, stream);
+    case 4: return dense_tile_launch<T, 2, 2, 3, 2, 3, 2>(p, k.splits, stream);
+    case 5: return dense_tile_launch<T, 4, 2, 1, 2, 4, 4>(p, k.splits, stream);
+    case 6: return dense_tile_launch<T, 2, 2, 2, 2, 4, 2>(p, k.splits, stream);
+    case 7: return dense_tile_launch<T, 2, 2, 1, 2, 6, 2>(p, k.splits, stream);
     default: return dense_tile_launch<T, 2, 2, 1, 1, 8, 2>(p, k.splits, stream);
   }
 }
