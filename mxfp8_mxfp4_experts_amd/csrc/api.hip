@@ -488,9 +488,9 @@ moe_status_t moe_int8_linear(const uint16_t* x, int64_t ld_x, const int8_t* w, c
   if (s != MOE_OK) return s;
   int8_t* xq = reinterpret_cast<int8_t*>(static_cast<char*>(workspace) + l.xq);
   float* xs = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.xs);
-  if (dense_fuses_quant(M, N, K))
+  if (const int q = dense_fused_q(M, N, K))
     return finish(launch_dense_quant(
-        int8_params(nullptr, K, nullptr, w, w_s, M, N, K, out_type, out, ld_out, workspace), x,
+        q, int8_params(nullptr, K, nullptr, w, w_s, M, N, K, out_type, out, ld_out, workspace), x,
         ld_x, stream));
   if (launch_norm(quant_params(x, ld_x, M, K, xq, l.ld_q, xs), MOE_Q8_INT8, false, stream) !=
       hipSuccess)

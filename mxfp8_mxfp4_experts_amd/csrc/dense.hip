@@ -141,22 +141,24 @@ __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_kernel(DensePa
   direct_finish<T, Q>(p, acc, m0, n0, red_s);
 }
 
-// INT8 with bf16 tokens, in one launch: the workgroup quantises its tokens (at
-// most 16 / Q, with the rule of moe_quant_int8) into LDS while its first weight
-// loads are on their way.  kUnits: units of 512 elements per wavefront.
+// INT8 with bf16 tokens, in one launch: the workgroup quantises its tokens (16 / Q,
+// with the rule of moe_quant_int8) into LDS while its first weight loads are on
+// their way.  kUnits: units of 512 elements per wavefront.
 template <int Q, int kBatch, int kUnits>
 __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_quant_kernel(
     DenseParams p, const uint16_t* __restrict__ x, int64_t ld_x) {
   using T = DenseI8;
   using G = DirectGeom<T, Q>;
-  extern __shared__ __attribute__((aligned(16))) uint8_t tok_s[];   // [M][K + 16]
+  extern __shared__ __attribute__((aligned(16))) uint8_t tok_s[];   // [tokens][K + 16]
   __shared__ v4i red_s[64 * kDirectWaves];
   __shared__ uint32_t max_s[kUnits * kDirectWaves];
   __shared__ float sx_s[16 / Q];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = (lane & 15) / Q, kq = lane % Q, g = lane >> 4;
-  const int n0 = blockIdx.x * G::kCols, K = p.Kb, M = p.M, pieces = K / 8, row_s = K + 16;
-  const int units = (pieces + 63) / 64;
+  const int n0 = blockIdx.x * G::kCols, m0 = blockIdx.y * G::kCols;
+  const int M = min(p.M - m0, G::kCols);
+  const int K = p.Kb, pieces = K / 8, row_s = K + 16, units = (pieces + 63) / 64;
+  x += m0 * ld_x;
   const int k0 = 64 * (Q * wave + kq) + 16 * g;
   const uint8_t* bp = p.b + (int64_t)min(n0 + c, p.N - 1) * p.ld_b;
   const v4i zero{0, 0, 0, 0};
@@ -215,6 +217,8 @@ __global__ __launch_bounds__(64 * kDirectWaves) void dense_direct_quant_kernel(
     for (int i = 0; i < kBatch; ++i) b[i] = next[i];
   }
   p.sx = sx_s;
+  p.M = M;
+  p.out = static_cast<uint8_t*>(p.out) + m0 * p.ld_out * (p.out_f32 ? 4 : 2);
   direct_finish<T, Q>(p, acc, 0, n0, red_s);
 }
 
@@ -242,14 +246,6 @@ int direct_q(int M, int N, int64_t Kb) {
     if (direct_ns(q, M, N, Kb) < direct_ns(best, M, N, Kb)) best = q;
   return best;
 }
-// For tokens quantised in the same launch: every workgroup quantises all of them,
-// so no more workgroups than CUs where N allows it.
-int fused_q(int M, int N) {
-  int q = 1;
-  while (q < 4 && M <= 8 / q && (N * (int64_t)(2 * q) + 15) / 16 <= kCus) q *= 2;
-  return q;
-}
-
 template <class T, int Q>
 hipError_t direct(const DenseParams& p, hipStream_t stream) {
   constexpr int C = 16 / Q;
@@ -275,25 +271,28 @@ hipError_t direct(const DenseParams& p, hipStream_t stream) {
   }
 }
 
-template <int Q>
+template <int Q, int kBatch>
 hipError_t direct_quant(const DenseParams& p, const uint16_t* x, int64_t ld_x,
                         hipStream_t stream) {
   constexpr int C = 16 / Q;
-  const dim3 grid((p.N + C - 1) / C), block(64 * kDirectWaves);
-  const size_t lds = (size_t)p.M * (p.Kb + 16);
-  const int steps = (p.Kb + DirectGeom<DenseI8, Q>::kStep - 1) / DirectGeom<DenseI8, Q>::kStep;
-  const bool one = p.M * ((p.Kb + 511) / 512) <= kDirectWaves;
-  if (steps <= 4 && one)
-    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 4, 1>), grid, block, lds, stream, p, x, ld_x);
-  else if (steps <= 4)
-    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 4, kFusedUnits>), grid, block, lds, stream, p,
-                       x, ld_x);
-  else if (one)
-    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 8, 1>), grid, block, lds, stream, p, x, ld_x);
+  const dim3 grid((p.N + C - 1) / C, (p.M + C - 1) / C), block(64 * kDirectWaves);
+  const int tokens = p.M < C ? p.M : C;
+  const size_t lds = (size_t)tokens * (p.Kb + 16);
+  if (tokens * ((p.Kb + 511) / 512) <= kDirectWaves)
+    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, kBatch, 1>), grid, block, lds, stream, p, x,
+                       ld_x);
   else
-    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, 8, kFusedUnits>), grid, block, lds, stream, p,
-                       x, ld_x);
+    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, kBatch, kFusedUnits>), grid, block, lds,
+                       stream, p, x, ld_x);
   return hipGetLastError();
+}
+template <int Q>
+hipError_t direct_quant(const DenseParams& p, const uint16_t* x, int64_t ld_x,
+                        hipStream_t stream) {
+  const int steps = (p.Kb + DirectGeom<DenseI8, Q>::kStep - 1) / DirectGeom<DenseI8, Q>::kStep;
+  if (steps <= 2) return direct_quant<Q, 2>(p, x, ld_x, stream);
+  if (steps <= 4) return direct_quant<Q, 4>(p, x, ld_x, stream);
+  return direct_quant<Q, 8>(p, x, ld_x, stream);
 }
 
 // The tiled kernel's variants, widest tile first: what one stage takes with at
@@ -318,8 +317,7 @@ constexpr int kNumVariants = sizeof(kVariants) / sizeof(kVariants[0]);
 constexpr int kMaxSplits = 16;
 constexpr int kDirectRows = 16;        // up to here always the direct kernel
 constexpr int kDirectMost = 512;       // up to here the direct kernel if it is estimated faster
-constexpr int kFusedRows = 8;          // tokens that the one-launch INT8 call quantises itself
-constexpr int kFusedBytes = 44 << 10;  // their codes in LDS, next to 16 KB of partial tiles
+constexpr int kFusedBytes = 44 << 10;  // a workgroup's codes in LDS, next to 16 KB of partial tiles
 
 // Most partial sums (4 bytes each) that a product of these sizes may use: grows
 // with M, so a workspace for M rows serves every smaller M.
@@ -332,34 +330,34 @@ int64_t most_partials(int M, int N) {
 struct Pick {
   int variant;   // -1: the direct kernel
   int splits;
+  float ns;      // estimated
 };
 
 // The kernel, variant and split of K with the least estimated time: whole rounds
 // of workgroups at their stage time, 2 us of launch, plus, with K split, a second
 // launch and the partial sums' way through the caches (11 bytes/ps).
 Pick pick(int M, int N, int64_t Kb) {
-  if (M <= kDirectRows) return {-1, 1};
+  Pick best{-1, 1, 3.4e38f};
+  if (M <= kDirectMost) best.ns = 1900.0f + direct_ns(direct_q(M, N, Kb), M, N, Kb);
+  if (M <= kDirectRows) return best;
   const int stages = (int)((Kb + kStageK - 1) / kStageK);
-  Pick best{-1, 1};
-  float least = M <= kDirectMost ? 1900.0f + direct_ns(direct_q(M, N, Kb), M, N, Kb) : 3.4e38f;
+  const float join = (float)M * N * 8 / 11000.0f;
+  const int64_t sums = (int64_t)M * ((N + 3) / 4 * 4);
+  // Splits are for launches that leave CUs idle; each has four stages at least.
+  int most = kMaxSplits < stages / 4 ? kMaxSplits : stages / 4;
+  while (most > 1 && most * sums > most_partials(M, N)) --most;
   for (int v = 0; v < kNumVariants; ++v) {
     const Variant& c = kVariants[v];
     const int64_t tiles = (int64_t)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
-    for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
-      // Splits are for launches that leave CUs idle.
-      if (s > 1 && (tiles * s > 2 * kCus || stages / s < 4 ||
-                    (int64_t)s * M * ((N + 3) / 4 * 4) > most_partials(M, N)))
-        break;
-      const int per = (stages + s - 1) / s;
-      const int64_t wgs = tiles * s, full = wgs / (kCus * c.per_cu), rest = wgs % (kCus * c.per_cu);
+    for (int s = 1; s == 1 || (s <= most && tiles * s <= 2 * kCus); ++s) {
+      const int per = (stages + s - 1) / s, at_once = kCus * c.per_cu;
+      const int64_t wgs = tiles * s;
+      const int rest = (int)(wgs & (at_once - 1));   // a power of two
       const float whole = per * (c.per_cu == 2 ? c.two : c.one) + c.fixed;
-      float t = 2000.0f + full * whole;
+      float t = 2000.0f + (float)(wgs >> (7 + c.per_cu)) * whole;
       if (rest) t += rest <= kCus ? per * c.one + c.fixed : whole;
-      if (s > 1) t += 1700.0f + (float)s * M * N * 8 / 11000.0f;
-      if (t < least) {
-        least = t;
-        best = {v, s};
-      }
+      if (s > 1) t += 1700.0f + s * join;
+      if (t < best.ns) best = {v, s, t};
     }
   }
   return best;
@@ -390,15 +388,34 @@ hipError_t launch(const DenseParams& p, hipStream_t stream) {
 
 size_t dense_workspace(int M, int N) { return sizeof(float) * (size_t)most_partials(M, N); }
 
-bool dense_fuses_quant(int M, int N, int K) {
-  if (M > 1 && (N + 15) / 16 > kCus) return false;
-  return M <= kFusedRows && M * ((K + 511) / 512) <= kFusedUnits * kDirectWaves &&
-         M * (K + 16) <= kFusedBytes;
+// One launch that quantises every workgroup's tokens anew, or two?  The estimate of
+// the one (fitted as those above to 258 products of 1 .. 1024 tokens, of which the
+// one launch is the faster for 160: 64 x 512 x 512 4.2 against 6.0 us, 256 x 240 x
+// 736 5.2 against 5.6, 28 x 2889 x 1104 8.2 against 6.6; the choice is 0.3% slower
+// than the better in the mean) against the other's plus 2.7 us for the quantisation, and half a
+// microsecond because a second launch costs the host 3.5 us.
+int dense_fused_q(int M, int N, int K) {
+  float least = 0.0f;
+  int best = 0;
+  for (int q = 1; q <= 4; q *= 2) {
+    const int c = 16 / q, tokens = M < c ? M : c, units = tokens * ((K + 511) / 512);
+    if (units > kFusedUnits * kDirectWaves || tokens * (K + 16) > kFusedBytes) continue;
+    if (M > 65535 * c) continue;   // the grid's second dimension
+    const int64_t wgs = (int64_t)((N + c - 1) / c) * ((M + c - 1) / c);
+    const float one = (float)(c + 2 * tokens) * K / 60.0f + (units > kDirectWaves ? 2100.0f : 1200.0f);
+    const float per_cu = (float)((wgs + kCus - 1) / kCus) * one, chip = (float)N * K / 5600.0f;
+    const float t = per_cu > chip ? per_cu : chip;
+    if (!best || t < least) {
+      least = t;
+      best = q;
+    }
+  }
+  return best && least <= pick(M, N, K).ns + 500.0f ? best : 0;
 }
 
-hipError_t launch_dense_quant(const DenseParams& p, const uint16_t* x, int64_t ld_x,
-                              hipStream_t stream) {
-  switch (fused_q(p.M, p.N)) {
+hipError_t launch_dense_quant(int q, const DenseParams& p, const uint16_t* x,
+                              int64_t ld_x, hipStream_t stream) {
+  switch (q) {
     case 1: return direct_quant<1>(p, x, ld_x, stream);
     case 2: return direct_quant<2>(p, x, ld_x, stream);
     default: return direct_quant<4>(p, x, ld_x, stream);

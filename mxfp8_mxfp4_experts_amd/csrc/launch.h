@@ -119,12 +119,12 @@ struct DenseParams {
   void* partial;            // dense_workspace bytes
 };
 size_t dense_workspace(int M, int N);   // grows with M
-// INT8 with bf16 tokens x in one launch (p.a and p.sx unused), for the sizes
-// that dense_fuses_quant accepts; the results of launch_norm's INT8
-// quantisation and launch_dense.
-bool dense_fuses_quant(int M, int N, int K);
-hipError_t launch_dense_quant(const DenseParams& p, const uint16_t* x, int64_t ld_x,
-                              hipStream_t stream);
+// INT8 with bf16 tokens x in one launch (p.a and p.sx unused): the results of
+// launch_norm's INT8 quantisation and launch_dense.  dense_fused_q: its Q for
+// these sizes, or 0 where the two launches are to be taken.
+int dense_fused_q(int M, int N, int K);
+hipError_t launch_dense_quant(int q, const DenseParams& p, const uint16_t* x,
+                              int64_t ld_x, hipStream_t stream);
 hipError_t launch_dense(bool i8, const DenseParams& p, hipStream_t stream);
 
 }  // namespace mi355moe

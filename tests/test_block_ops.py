@@ -182,6 +182,30 @@ gpu = pytest.mark.gpu
 
 
 @gpu
+@pytest.mark.parametrize("M,N,K", [(9, 33, 16), (16, 896, 1024), (17, 64, 512), (33, 131, 528),
+                                   (64, 512, 512), (15, 70, 2048), (24, 40, 3600), (28, 66, 1104),
+                                   (130, 77, 176), (257, 18, 272), (5, 9, 7168)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_int8_linear_equals_its_two_calls(M, N, K, out_dtype):
+    """One launch or two, with one block of tokens or several: the same bits
+    (also where a token holds a NaN), into rows of a wider buffer."""
+    import mxfp8_mxfp4_experts_amd as m
+    g = torch.Generator().manual_seed(M * N + K)
+    x = torch.randn(M, K, generator=g).bfloat16()
+    x[M // 2, K - 1] = NAN
+    x = torch.cat([x, x], 1).cuda()[:, :K]
+    w = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int8).cuda()
+    sw = torch.rand(N, generator=g).cuda()
+    q, s = m.moe_quant_int8(x)
+    want = m.moe_int8_matmul(q, s, w, sw, out_dtype=out_dtype)
+    wide = torch.full((M, N + 24), 7.0, dtype=out_dtype, device="cuda")
+    got = m.moe_int8_linear(x, w, sw, out=wide[:, :N])
+    assert torch.equal(got.isnan(), want.isnan()) and want.isnan().any(1).sum() == 1
+    assert torch.equal(got.nan_to_num(0), want.nan_to_num(0))
+    assert (wide[:, N:] == 7).all()
+
+
+@gpu
 def test_binding_refusals():
     """What the compiled checks refuse is named by the binding."""
     import mxfp8_mxfp4_experts_amd as m
