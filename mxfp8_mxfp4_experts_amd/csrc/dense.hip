@@ -18,7 +18,10 @@ namespace mi355moe {
 
 namespace {
 
-// Few rows: no operand is used twice enough to pay for LDS.  A workgroup of W
+// Few rows: no operand is used twice enough to pay for LDS, and the weights' one
+// way from memory bounds the product (INT8 1 x 3584 x 7168: 25.7 MB in 7.3 us, 3.5
+// TB/s with the launch; BF16 8 x 896 x 7168: 5.0 us, the chain of load, products
+// and join).  A workgroup of W
 // wavefronts owns 16 / Q output columns and 16 / Q tokens and splits K over its
 // wavefronts, each feeding the matrix unit straight from global loads, with the
 // loads of several steps in flight; the partial tiles are added through LDS in
@@ -388,12 +391,12 @@ hipError_t launch(const DenseParams& p, hipStream_t stream) {
 
 size_t dense_workspace(int M, int N) { return sizeof(float) * (size_t)most_partials(M, N); }
 
-// One launch that quantises every workgroup's tokens anew, or two?  The estimate of
-// the one (fitted as those above to 258 products of 1 .. 1024 tokens, of which the
-// one launch is the faster for 160: 64 x 512 x 512 4.2 against 6.0 us, 256 x 240 x
-// 736 5.2 against 5.6, 28 x 2889 x 1104 8.2 against 6.6; the choice is 0.3% slower
-// than the better in the mean) against the other's plus 2.7 us for the quantisation, and half a
-// microsecond because a second launch costs the host 3.5 us.
+// One launch that quantises every workgroup's tokens anew, or two?  The estimate
+// of the one (fitted as those above, to 258 products of 1 .. 1024 tokens, 160 of
+// them faster in one launch: 64 x 512 x 512 4.2 against 6.0 us, 256 x 240 x 736 5.2
+// against 5.6, 28 x 2889 x 1104 8.2 against 6.6) against the other's with 2.7 us
+// for the quantisation, and half a microsecond because a second launch costs the
+// host 3.5 us.  On 128 other products the choice is 1.3% slower than the better.
 int dense_fused_q(int M, int N, int K) {
   float least = 0.0f;
   int best = 0;
@@ -402,7 +405,8 @@ int dense_fused_q(int M, int N, int K) {
     if (units > kFusedUnits * kDirectWaves || tokens * (K + 16) > kFusedBytes) continue;
     if (M > 65535 * c) continue;   // the grid's second dimension
     const int64_t wgs = (int64_t)((N + c - 1) / c) * ((M + c - 1) / c);
-    const float one = (float)(c + 2 * tokens) * K / 60.0f + (units > kDirectWaves ? 2100.0f : 1200.0f);
+    const float first = units > kDirectWaves ? 2100.0f : 1200.0f;
+    const float one = (float)(c + 2 * tokens) * K / 60.0f + first;
     const float per_cu = (float)((wgs + kCus - 1) / kCus) * one, chip = (float)N * K / 5600.0f;
     const float t = per_cu > chip ? per_cu : chip;
     if (!best || t < least) {

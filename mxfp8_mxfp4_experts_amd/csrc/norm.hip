@@ -13,6 +13,10 @@
 // reduction and the outputs.  Rounding is monotone, so the largest |y| is the
 // largest |h * w| times rstd exactly, and the sum of squares and the absolute
 // maximum are reduced together with one barrier.
+//
+// Memory bounds it at many rows (8192 x 7168 with a residual and MXFP8: 530 MB in
+// 92.9 us, 5.7 TB/s; INT8 quantisation alone 176 MB in 31 us), the chain of load,
+// reduction and stores at few (one row 3.4 us).
 #include "common.h"
 #include "launch.h"
 #include "q8_dev.h"

@@ -35,6 +35,10 @@
 // groups' worths are taken exactly, again from candidates only.  With more than
 // 64 candidates, or NaN or huge keys, the wavefront evaluates everything
 // exactly.
+//
+// Vector instructions bound it at many tokens, about 790 a token and wavefront
+// (8192 x 896, 8 groups of which 4, top 16: 52.9 us with every score exact, 16.1
+// narrowed; 30 MB, 1.9 TB/s), and one wavefront's chain at few (8 tokens: 6.0 us).
 #include "common.h"
 #include "launch.h"
 #include "route_dev.h"
