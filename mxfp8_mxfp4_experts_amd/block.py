@@ -12,7 +12,9 @@ In order, on the current stream:
 The block's output is the experts' share only: the caller adds it to h, which
 the next block's norm does on its way in (pass it as that block's ``x`` and h as
 its ``residual``).  Buffers are allocated once for ``max_tokens`` and reused, so
-a call allocates nothing but its two outputs.
+a call allocates nothing but its two outputs, and a graph captured with up to
+``max_tokens`` stays valid whatever such batches run beside it.  A larger batch
+makes the buffers anew: graphs from before it are to be captured again.
 """
 from __future__ import annotations
 
@@ -76,16 +78,10 @@ class MoEBlock:
             self.z = torch.empty((T, L), dtype=torch.bfloat16, device=dev)
             self.z_out = torch.empty((T, L), dtype=torch.bfloat16, device=dev)
         # One workspace for all products: each runs after the one before on the stream.
-        self.workspace = torch.empty(0, dtype=torch.uint8, device=dev)
-
-    def _workspace(self, T: int) -> torch.Tensor:
-        need = B.moe_gate_workspace_size(T, self.E, self.H)
+        need = B.moe_gate_workspace_size(T, self.E, H)
         if self.down is not None:
-            need = max(need, B.moe_int8_workspace_size(T, self.L, self.H),
-                       B.moe_int8_workspace_size(T, self.H, self.L))
-        if self.workspace.numel() < need:
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-        return self.workspace
+            need = max(need, B.moe_int8_workspace_size(T, L, H), B.moe_int8_workspace_size(T, H, L))
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
 
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
                  out: Optional[torch.Tensor] = None,
@@ -100,7 +96,7 @@ class MoEBlock:
             x, self.norm_w, self.eps, residual=residual,
             q8=B.Q8_MXFP8 if self.down is None else B.Q8_INT8, residual_out=residual_out, y=y,
             xq=xq, xs=xs)
-        ws = self._workspace(T)
+        ws = self.workspace
         logits = B.moe_gate_logits(y, self.gate_w, out=self.logits[:T], workspace=ws)
         idx, w = B.moe_route_groups(
             logits, self.gate_bias, self.experts.top_k, n_group=self.n_group,
