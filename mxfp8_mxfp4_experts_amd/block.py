@@ -34,6 +34,8 @@ class MoEBlock:
                  down: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
                  up: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, max_tokens: int = 1):
         """norm_w bf16 [H]; gate_w bf16 [E, H]; gate_bias float [E] or None.
+        ``experts``, where made for fewer than ``max_tokens``, gives its weights
+        only: the block then has a layer with buffers of its own.
         ``down`` / ``up``: (int8 [L, H], float [L]) into the experts' width L and
         (int8 [H, L], float [H]) back, both or none, as ``quantise`` gives them."""
         self.experts, self.norm_w, self.gate_w, self.gate_bias = experts, norm_w, gate_w, gate_bias
@@ -65,6 +67,11 @@ class MoEBlock:
     def _alloc(self, T: int):
         dev, H, L = self.device, self.H, self.L
         self.max_tokens = T
+        if self.experts.max_tokens < T:
+            # Else the layer would make its buffers anew in the middle of the block's calls, and
+            # graphs that use them, captured of the block or of the layer itself, would write to
+            # memory given back.
+            self.experts = self.experts.with_max_tokens(T)
         self.y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
         self.logits = torch.empty((T, self.E), dtype=torch.float32, device=dev)
         self.topk_idx = torch.empty((T, self.experts.top_k), dtype=torch.int32, device=dev)

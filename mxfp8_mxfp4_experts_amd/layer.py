@@ -2,7 +2,9 @@
 
 Buffers (routing outputs, MXFP8 activations, grouping, FC1 output and the
 workspace) are allocated once for ``max_tokens`` and reused, so a call
-allocates nothing but its output (or nothing when ``out`` is given).
+allocates nothing but its output (or nothing when ``out`` is given).  A larger
+batch makes the buffers anew: graphs from before it are to be captured again
+(``with_max_tokens`` gives a layer with larger ones beside this one's).
 
 With ``tiled=True`` (the default where the shapes allow it: I % 256 == 0 and
 H % 512 == 0) the weights are reordered once into the library's tiled layout
@@ -68,6 +70,14 @@ class MoELayer:
         other.__dict__.update(self.__dict__)
         other.combine_mode = B.COMBINE_ATOMIC if combine == "atomic" else B.COMBINE_DETERMINISTIC
         other._alloc(self.max_tokens)
+        return other
+
+    def with_max_tokens(self, max_tokens: int) -> "MoELayer":
+        """A layer sharing these (already prepacked) weights, with buffers of
+        its own for ``max_tokens``; this one's stay as they are."""
+        other = object.__new__(MoELayer)
+        other.__dict__.update(self.__dict__)
+        other._alloc(max_tokens)
         return other
 
     def _alloc(self, T: int):

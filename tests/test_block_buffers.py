@@ -59,18 +59,19 @@ def cpu_layer(H, I, E, K, max_tokens):
     return layer
 
 
-def cpu_block(H, L, E=64, K=4, max_tokens=MOST):
+def cpu_block(H, L, E=64, K=4, max_tokens=MOST, layer_tokens=MOST):
     pair = lambda n, k: (torch.empty(n, k, dtype=torch.int8), torch.empty(n))  # noqa: E731
     kw = dict(down=pair(L, H), up=pair(H, L)) if L != H else {}
-    return MoEBlock(cpu_layer(L, 256, E, K, max_tokens), torch.empty(H, dtype=torch.bfloat16),
+    return MoEBlock(cpu_layer(L, 256, E, K, layer_tokens), torch.empty(H, dtype=torch.bfloat16),
                     torch.empty(E, H, dtype=torch.bfloat16), max_tokens=max_tokens, **kw)
 
 
 @pytest.mark.parametrize("H,L", [(1024, 1024), (2048, 512)])
-def test_buffers_stay_for_every_batch_up_to_max_tokens(monkeypatch, H, L):
+@pytest.mark.parametrize("layer_tokens", [MOST, 1])
+def test_buffers_stay_for_every_batch_up_to_max_tokens(monkeypatch, H, L, layer_tokens):
     """Whatever the order of batches, each call is given the same memory, and enough of it."""
     calls = Calls(monkeypatch)
-    block = cpu_block(H, L)
+    block = cpu_block(H, L, layer_tokens=layer_tokens)
     first = calls.of(block, 1)
     assert len(first) >= 5
     for T in (64, 5, MOST, 17, 256):
@@ -80,9 +81,24 @@ def test_buffers_stay_for_every_batch_up_to_max_tokens(monkeypatch, H, L):
             assert calls.sizes["moe_int8_linear"] >= B.moe_int8_workspace_size(T, H, L)
 
 
+def test_a_smaller_layer_keeps_its_buffers(monkeypatch):
+    """A layer for fewer tokens than the block's is left as it is: graphs of its own stay valid."""
+    calls = Calls(monkeypatch)
+    layer = cpu_layer(512, 256, 64, 4, 8)
+    before = {k: v.data_ptr() for k, v in vars(layer).items() if isinstance(v, torch.Tensor)}
+    block = MoEBlock(layer, torch.empty(512, dtype=torch.bfloat16),
+                     torch.empty(64, 512, dtype=torch.bfloat16), max_tokens=64)
+    calls.of(block, 64)
+    calls.of(block, 200)                                   # past max_tokens: the block's grow
+    assert block.max_tokens == 200
+    after = {k: v.data_ptr() for k, v in vars(layer).items() if isinstance(v, torch.Tensor)}
+    assert after == before and layer.max_tokens == 8
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("H,L", [(512, 512), (4096, 512)])
-def test_graph_of_a_block_beside_larger_batches(H, L):
+@pytest.mark.parametrize("layer_tokens", [MOST, 1])
+def test_graph_of_a_block_beside_larger_batches(H, L, layer_tokens):
     """A block captured at 64 tokens, larger batches run eagerly between the replays: every replay
     gives the eager result, and memory taken meanwhile keeps its contents."""
     import synth
@@ -91,7 +107,7 @@ def test_graph_of_a_block_beside_larger_batches(H, L):
     cfg = synth.custom_config("block_graph", 811, T=T, H=L, I=256, E=E, K=K)
     w = {k: v.to(dev) for k, v in synth.make_expert_weights(cfg, device="cpu").items()}
     layer = MoELayer(w["w13"], w["w13_s"], w["w2"], w["w2_s"], top_k=K, E=E,
-                     max_tokens=MOST)
+                     max_tokens=layer_tokens)
     g = torch.Generator().manual_seed(5)
 
     def rand(*shape, scale=1.0):
