@@ -399,9 +399,15 @@ moe_status_t moe_quant_int8(const uint16_t* x, int64_t ld_x, int T, int H, int8_
                             float* xs, hipStream_t stream);
 
 /* Bytes of workspace for moe_int8_linear (and so for moe_int8_matmul) with
- * these sizes; it grows with M, so a buffer for M rows serves every smaller M
- * with the same N and K.  0 for invalid sizes. */
+ * these sizes: the product's partial sums, and the tokens in 8 bits with their
+ * scales.  It grows with M, so a buffer for M rows serves every smaller M with
+ * the same N and K.  0 for invalid sizes. */
 size_t moe_int8_workspace_size(int M, int N, int K);
+
+/* Bytes of workspace for moe_int8_matmul alone, whose tokens are in 8 bits
+ * already: the partial sums, at most 16 MB.  It grows with M.  0 for M = 0 and
+ * for invalid sizes. */
+size_t moe_int8_matmul_workspace_size(int M, int N, int K);
 
 /* out[m, n] = (sum_k xq[m, k] * w[n, k]) * xs[m] * w_s[n]: the sum exact in
  * int32, the three factors multiplied in float in this order, one rounding to
@@ -412,15 +418,15 @@ size_t moe_int8_workspace_size(int M, int N, int K);
  *        aligned (bf16) or 4-byte aligned (float); vector stores where ld_out
  *        is a multiple of 4 and out is 16-byte aligned.
  *   K a multiple of 16, 16 <= K <= 131056 (no int32 overflow); 1 <= N <= 2^20.
- *   workspace  at least moe_int8_workspace_size bytes, 256-byte aligned. */
+ *   workspace  at least moe_int8_matmul_workspace_size bytes, 256-byte aligned. */
 moe_status_t moe_int8_matmul(const int8_t* xq, int64_t ld_xq, const float* xs, const int8_t* w,
                              const float* w_s, int M, int N, int K, int out_type, void* out,
                              int64_t ld_out, void* workspace, size_t ws_bytes,
                              hipStream_t stream);
 
 /* moe_quant_int8 of x [M, K] (bf16 bits, row stride ld_x), then
- * moe_int8_matmul of the result (kept in the workspace): same output.  K at
- * most 32768. */
+ * moe_int8_matmul of the result (kept in the workspace, which has at least
+ * moe_int8_workspace_size bytes): same output.  K at most 32768. */
 moe_status_t moe_int8_linear(const uint16_t* x, int64_t ld_x, const int8_t* w, const float* w_s,
                              int M, int N, int K, int out_type, void* out, int64_t ld_out,
                              void* workspace, size_t ws_bytes, hipStream_t stream);

@@ -32,6 +32,7 @@ from ._binding import (  # noqa: F401
     moe_gate_workspace_size,
     moe_int8_linear,
     moe_int8_matmul,
+    moe_int8_matmul_workspace_size,
     moe_int8_workspace_size,
     moe_permute,
     moe_permute_noalloc,

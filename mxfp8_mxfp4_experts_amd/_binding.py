@@ -29,8 +29,9 @@ EXPORTS = (
     "moe_permute", "moe_fc1_situ", "moe_fc2_combine", "moe_prepack_w13", "moe_prepack_w2",
     "moe_fc1_situ_tiled", "moe_fc2_combine_tiled", "moe_route_quant_permute",
     "moe_prepack_w13_layout", "moe_permute_noalloc", "moe_quant_permute",
-    "moe_add_rmsnorm", "moe_quant_int8", "moe_int8_workspace_size", "moe_int8_matmul",
-    "moe_int8_linear", "moe_gate_workspace_size", "moe_gate_logits", "moe_route_groups",
+    "moe_add_rmsnorm", "moe_quant_int8", "moe_int8_workspace_size",
+    "moe_int8_matmul_workspace_size", "moe_int8_matmul", "moe_int8_linear",
+    "moe_gate_workspace_size", "moe_gate_logits", "moe_route_groups",
 )
 
 # moe_w13_layout_t values (row order of a w13 tensor)
@@ -98,7 +99,8 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
                                     _P, _P, _P]
     lib.moe_quant_int8.restype = _I
     lib.moe_quant_int8.argtypes = [_P, _I64, _I, _I, _P, _P, _P]
-    for name in ("moe_int8_workspace_size", "moe_gate_workspace_size"):
+    for name in ("moe_int8_workspace_size", "moe_int8_matmul_workspace_size",
+                 "moe_gate_workspace_size"):
         getattr(lib, name).restype = _SZ
         getattr(lib, name).argtypes = [_I, _I, _I]
     lib.moe_int8_matmul.restype = _I
@@ -634,6 +636,12 @@ def moe_int8_workspace_size(M: int, N: int, K: int) -> int:
     return n
 
 
+def moe_int8_matmul_workspace_size(M: int, N: int, K: int) -> int:
+    """Workspace bytes of moe_int8_matmul alone; a buffer for M rows serves
+    fewer."""
+    return lib().moe_int8_matmul_workspace_size(M, N, K)
+
+
 def _int8_out(out, out_dtype, M, N, idx):
     """The output tensor, its address, row stride and moe_out_t value."""
     if out is None:
@@ -679,7 +687,7 @@ def moe_int8_matmul(xq, xs, w, w_s, out=None, out_dtype=torch.bfloat16, workspac
     N, w_p, s_p = _int8_weight(w, w_s, K, idx)
     out, o_p, ld_out, kind = _int8_out(out, out_dtype, M, N, idx)
     L = _lib or lib()
-    workspace = _workspace(workspace, L.moe_int8_workspace_size, (M, N, K), idx)
+    workspace = _workspace(workspace, L.moe_int8_matmul_workspace_size, (M, N, K), idx)
     st = L.moe_int8_matmul(q_p, ld_xq, x_p, w_p, s_p, M, N, K, kind, o_p, ld_out,
                            workspace.data_ptr(), workspace.numel(), _raw_stream(idx))
     if st:

@@ -87,7 +87,8 @@ class MoEBlock:
         # One workspace for all products: each runs after the one before on the stream.
         need = B.moe_gate_workspace_size(T, self.E, H)
         if self.down is not None:
-            need = max(need, B.moe_int8_workspace_size(T, L, H), B.moe_int8_workspace_size(T, H, L))
+            need = max(need, B.moe_int8_matmul_workspace_size(T, L, H),
+                       B.moe_int8_workspace_size(T, H, L))
         self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
 
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,

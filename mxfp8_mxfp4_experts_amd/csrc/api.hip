@@ -451,6 +451,11 @@ size_t moe_int8_workspace_size(int M, int N, int K) {
   return int8_layout(M, N, K).total;
 }
 
+size_t moe_int8_matmul_workspace_size(int M, int N, int K) {
+  if (!valid_int8(M, N, K)) return 0;
+  return int8_layout(M, N, K).xq;
+}
+
 moe_status_t moe_int8_matmul(const int8_t* xq, int64_t ld_xq, const float* xs, const int8_t* w,
                              const float* w_s, int M, int N, int K, int out_type, void* out,
                              int64_t ld_out, void* workspace, size_t ws_bytes,
