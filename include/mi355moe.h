@@ -445,10 +445,14 @@ moe_status_t moe_gate_logits(const uint16_t* x, int64_t ld_x, const uint16_t* w,
                              size_t ws_bytes, hipStream_t stream);
 
 /* Routing with groups of experts.
- *   score: s_e = sigmoid(l_e), or exp(l_e - max) / sum over the unmasked
- *   experts, evaluated in double and rounded once to float.  key_e = s_e +
- *   bias_e in float (bias NULL: s_e).  An expert is masked for a token when its
- *   logit is -inf or the lowest finite float, or its key is -inf.
+ *   score: s_e = sigmoid(l_e), or exp(l_e - max) / sum over the experts that
+ *   their logits do not mask, evaluated in double and rounded once to float.
+ *   key_e = s_e + bias_e in float (bias NULL: s_e).  An expert is masked for a
+ *   token when its logit is -inf or the lowest finite float, or its key is
+ *   -inf.  The bias takes part in the choice only: an expert whose bias is -inf
+ *   is never taken but keeps its share of the softmax, so that the weights of
+ *   the others do not depend on biases (without renormalise they then add up to
+ *   less than without that expert).
  *   The experts stand in n_group groups of E / n_group neighbours; the
  *   topk_group groups of most worth (group_score; masked experts do not count)
  *   stay, and of their experts the top_k with the largest keys, in descending

@@ -2,8 +2,9 @@
 // that only takes part in the choice, the best groups of experts, then the
 // best experts in them, weights renormalised or not.
 //
-//   s_e   = sigmoid(l_e), or exp(l_e - max) / sum (over the unmasked experts),
-//           evaluated in double and rounded once to float
+//   s_e   = sigmoid(l_e), or exp(l_e - max) / sum (over the experts that their
+//           logits do not mask, whatever their biases), evaluated in double and
+//           rounded once to float
 //   key_e = s_e + bias_e (float); an expert is masked when l_e is -inf or the
 //           lowest finite float, or its key is -inf
 //   worth of a group: its best key, or the float sum of its best two
