@@ -124,8 +124,8 @@ PROBE_OUT = os.path.join(PROBE_DIR, "libnumprobe.so")
 
 def build_probes(verbose: bool = False) -> str:
     """The test-only probe library (device functions of the FC kernels run
-    on inputs the GPU tests choose)."""
-    return _build_so([os.path.join(PROBE_DIR, "numerics_probe.hip")], PROBE_OUT, "probe",
+    on inputs the GPU tests choose, and which kernel a dense product takes)."""
+    return _build_so(sorted(glob.glob(os.path.join(PROBE_DIR, "*.hip"))), PROBE_OUT, "probe",
                      verbose)
 
 

@@ -33,10 +33,10 @@
 #pragma once
 
 #include "dense.h"
+#include "dense_pick.h"
 
 namespace mi355moe {
 
-constexpr int kStageK = 128;                    // bytes of K per stage
 constexpr uint32_t kPastEnd = 0x80000000u;      // beyond every buffer (they are below 2^31 bytes)
 
 typedef __attribute__((address_space(3))) uint8_t dense_lds_t;

@@ -427,8 +427,9 @@ def int8_case(seed, M, N, K):
     return q, sx, w, sw
 
 
-# tokens on both sides of every tile height, widths on both sides of every tile width, K with and
-# without a rest below one stage
+# Tokens from one to 300 and more, odd widths, K with and without a rest below one stage: mostly the
+# direct kernel and the small tiles (every variant and split has its shapes in
+# test_dense_variants.py).
 INT8_SHAPES = [(1, 1, 16), (1, 17, 48), (2, 16, 64), (15, 33, 112), (16, 64, 128), (17, 5, 144),
                (31, 100, 256), (33, 129, 272), (48, 224, 1040), (63, 255, 512), (65, 257, 640),
                (100, 96, 4096), (127, 448, 400), (129, 449, 1008), (255, 31, 2064),

@@ -10,8 +10,13 @@ pytestmark = pytest.mark.gpu
 LOWEST = -3.4028234663852886e38
 
 
-@pytest.mark.parametrize("E,K,G,KG", [(16, 8, 1, 1), (64, 6, 8, 3), (896, 16, 8, 4),
-                                      (2048, 16, 1, 1), (1056, 12, 4, 3)])
+# Experts per lane on both sides of 2, 4, 8 and 16, one and several groups.
+SHAPES = [(16, 8, 1, 1), (64, 6, 8, 3), (128, 8, 1, 1), (130, 6, 2, 1), (256, 8, 1, 1),
+          (300, 8, 1, 1), (512, 8, 1, 1), (576, 8, 1, 1), (896, 16, 8, 4), (1024, 16, 1, 1),
+          (1088, 9, 1, 1), (2048, 16, 1, 1), (1056, 12, 4, 3)]
+
+
+@pytest.mark.parametrize("E,K,G,KG", SHAPES)
 def test_bias_of_minus_infinity_keeps_its_share_of_the_softmax(E, K, G, KG):
     """The weights are softmax values over every expert that its logit does not mask; a bias of
     -inf takes an expert out of the choice only.  Expected values by torch.softmax in 64 bits."""
