@@ -255,12 +255,17 @@ hipError_t direct_quant(const DenseParams& p, const uint16_t* x, int64_t ld_x,
   const dim3 grid((p.N + C - 1) / C, (p.M + C - 1) / C), block(64 * kDirectWaves);
   const int tokens = p.M < C ? p.M : C;
   const size_t lds = (size_t)tokens * (p.Kb + 16);
-  if (tokens * ((p.Kb + 511) / 512) <= kDirectWaves)
-    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, kBatch, 1>), grid, block, lds, stream, p, x,
-                       ld_x);
-  else
-    hipLaunchKernelGGL((dense_direct_quant_kernel<Q, kBatch, kFusedUnits>), grid, block, lds,
-                       stream, p, x, ld_x);
+  // One unit per wavefront reaches K = 8192, where batches of 4 are for more than 2048 Q and of 8
+  // for more than 4096 Q.
+  if constexpr (kBatch == 2 || kBatch * Q < 16) {
+    if (tokens * ((p.Kb + 511) / 512) <= kDirectWaves) {
+      hipLaunchKernelGGL((dense_direct_quant_kernel<Q, kBatch, 1>), grid, block, lds, stream, p, x,
+                         ld_x);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((dense_direct_quant_kernel<Q, kBatch, kFusedUnits>), grid, block, lds, stream,
+                     p, x, ld_x);
   return hipGetLastError();
 }
 template <int Q>

@@ -116,6 +116,9 @@ def test_direct_shapes(probe):
 
 
 def test_fused_shapes(probe):
+    # One unit per wavefront ends at K = 8192, where the longer batches begin for larger Q.
+    assert set(FUSED) == {(q, b, more) for q in (1, 2, 4) for b in (2, 4, 8)
+                          for more in (False, True) if more or b == 2 or b * q < 16}
     for (q, b, more), shapes in FUSED.items():
         for M, N, K in shapes:
             assert probe.probe_fused_q(M, N, K) == q, (M, N, K)
