@@ -87,7 +87,8 @@ ARGS_OUT = os.path.join(PKG, "_tensor_args.so")
 
 def build_args(verbose: bool = False) -> str:
     """The binding's argument checks ``_tensor_args.so`` (host code against
-    torch's headers)."""
+    torch's headers, by the compiler that builds the library: no other is
+    needed)."""
     import sysconfig
 
     import torch
@@ -95,7 +96,8 @@ def build_args(verbose: bool = False) -> str:
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = ARGS_OUT + ".tmp"
-    rc, out = _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+    rc, out = _run([HIPCC, "-x", "c++", "-no-hip-rt", "-O2", "-std=c++17", "-shared", "-fPIC",
+                    "-Wall",
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
                     "-I", sysconfig.get_paths()["include"], "-isystem", inc, "-isystem",
                     os.path.join(inc, "torch", "csrc", "api", "include"), ARGS_SRC, "-L", libs,
@@ -103,7 +105,7 @@ def build_args(verbose: bool = False) -> str:
     if rc != 0 or (out.strip() and verbose):
         print(f"[build] tensor_args.cpp:\n{out}", file=sys.stderr)
     if rc != 0:
-        raise RuntimeError("g++ failed; see messages above")
+        raise RuntimeError("hipcc failed on tensor_args.cpp; see messages above")
     os.replace(tmp, ARGS_OUT)
     return ARGS_OUT
 
