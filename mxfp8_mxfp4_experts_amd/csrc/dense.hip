@@ -20,9 +20,9 @@ namespace mi355moe {
 namespace {
 
 // Few rows: no operand is used twice enough to pay for LDS, and the weights' one
-// way from memory bounds the product (INT8 1 x 3584 x 7168: 25.7 MB in 7.3 us, 3.5
-// TB/s with the launch; BF16 8 x 896 x 7168: 5.0 us, the chain of load, products
-// and join).  A workgroup of W
+// way from memory bounds the product (INT8 1 x 3584 x 7168: 25.7 MB in 7.2 - 8.0 us,
+// 3.2 - 3.6 TB/s with the launch; BF16 8 x 896 x 7168: 5.7 - 6.1 us, the chain of
+// load, products and join).  A workgroup of W
 // wavefronts owns 16 / Q output columns and 16 / Q tokens and splits K over its
 // wavefronts, each feeding the matrix unit straight from global loads, with the
 // loads of several steps in flight; the partial tiles are added through LDS in

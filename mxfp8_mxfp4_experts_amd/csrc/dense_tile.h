@@ -24,12 +24,15 @@
 // Rows past M or N, chunks past K and stages past the last are loads beyond
 // the buffer's end: they bring zeros, touch no memory and still count.
 //
-// Measured: INT8 8192 x 3584 x 7168 in 256 x 224 tiles 169 - 180 us (2.3 - 2.5
-// POP/s; the matrix unit is busy 58% of the cycles at a clock that the power
-// limit holds at 2.0 GHz), BF16 8192 x 896 x 7168 in 128 x 224 tiles 99 us (1.06
-// PFLOP/s; 1.3 GB out of the L2s bound it), INT8 256 x 3584 x 7168 in 64 x 64
-// tiles 14 us, BF16 256 x 896 x 7168 with K in four 9.6 us and its join 2.2: the
-// latter two take 60 - 85 bytes/ns per CU from L2, which bounds them.
+// Measured (least and median of 60 launches under a trace, which the large ones
+// feel): INT8 8192 x 3584 x 7168 in 256 x 224 tiles 176 - 188 us (2.2 - 2.4 POP/s;
+// the matrix unit is busy 58% of the cycles at a clock that the power limit holds
+// at 2.0 GHz); BF16 8192 x 896 x 7168 in 128 x 224 tiles 110 - 118 us, 100 in calls
+// back to back (1.06 PFLOP/s; what bounds it is open: 1.3 GB out of the L2s is 51
+// bytes/ns per CU, less than smaller tiles draw); INT8 256 x 3584 x 7168 in 64 x 64
+// tiles 14.3 - 15.9 us; BF16 256 x 896 x 7168 with K in four 9.6 - 10.0 us and its
+// join 2.2 - 2.7: the latter two take 60 - 85 bytes/ns per CU from L2, which bounds
+// them.
 #pragma once
 
 #include "dense.h"

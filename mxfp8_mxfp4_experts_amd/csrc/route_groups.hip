@@ -22,7 +22,7 @@
 //     Sigmoid: the exponent's argument rounds by |l| 2^-24 relative, which is
 //     s(1-s)|l| 2^-24 < 2^-26 of the score, v_exp_f32's ulp s(1-s) 2^-23 <=
 //     2^-25, the sum and the rounding of the exact score 2^-24 and 2^-25,
-//     v_rcp_f32's ulp 2^-23: below 2^-22 together.  Softmax: two roundings of the
+//     v_rcp_f32's ulp 2^-23: 17/16 of 2^-22 together.  Softmax: two roundings of the
 //     argument x, p|x| 2^-23 < 2^-24, exponential, scale and product 2^-23 +
 //     2^-24 + 2^-24, the exact score's 2^-25: below 2^-21.5;
 //   * a key adds bias in float, rounding by at most 2^-24 |key| on each side
@@ -35,11 +35,17 @@
 // within their errors (about one token in 3000 at 896 experts in 8 groups), the
 // groups' worths are taken exactly, again from candidates only.  With more than
 // 64 candidates, or NaN or huge keys, the wavefront evaluates everything
-// exactly.
+// exactly; likewise where a lane has more than 16 experts, whose keys would not
+// stay in registers (one group: 8192 x 1024 14.5 us, 8192 x 1056 66, 8192 x 2048
+// 123, 8192 x 4096 439; 9 groups of 99, 25 experts a lane, 37).
+//
+// The exact path's sum of exponentials runs in another order than the narrowed
+// one's, both in double: a softmax score next to a rounding boundary of float may
+// so differ by its last bit between the two; sigmoid scores are the same.
 //
 // Vector instructions bound it at many tokens, about 790 a token and wavefront
-// (8192 x 896, 8 groups of which 4, top 16: 52.9 us with every score exact, 16.1
-// narrowed; 30 MB, 1.9 TB/s), and one wavefront's chain at few (8 tokens: 6.0 us).
+// (8192 x 896, 8 groups of which 4, top 16: 52.9 us with every score exact, 16.3
+// narrowed; 30 MB, 1.9 TB/s), and one wavefront's chain at few (8 tokens: 6.1 us).
 #include "common.h"
 #include "launch.h"
 #include "route_dev.h"
