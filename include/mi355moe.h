@@ -478,6 +478,122 @@ moe_status_t moe_route_groups(const float* logits, int64_t ld_logits, const floa
                               int group_score, int renormalise, float routed_scaling,
                               int32_t* topk_idx, float* topk_w, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Products in 8-bit floating point with a scale for each block of 128 (the
+ * format of checkpoints that store E4M3 weights beside one float per block of
+ * 128 x 128).  Additions to ABI version 3; the conventions above hold.
+ *
+ *   moe_quant_fp8    bf16 tokens -> E4M3, one float per token and 128 elements
+ *   moe_fp8_matmul, moe_fp8_linear    dense, from E4M3 and from bf16 tokens
+ *   moe_fp8_grouped  the rows of every expert times that expert's weight
+ *
+ * Blocks: KB = ceil(K / 128) along the contraction, NB = ceil(N / 128) along
+ * the weight's rows; the last block of either may be shorter.
+ *   xq   E4M3 [M, K], row stride ld_xq (>= K, a multiple of 16).
+ *   xs   float [KB, M], row stride ld_xs (>= M): the scale of token m's block b
+ *        is xs[b, m] (tokens side by side: the products read one block of many
+ *        tokens at a time).
+ *   w    E4M3 [N, K]; w_s float [NB, KB]; experts one after another.
+ *   out  bf16 [M, N], row stride ld_out (>= N), 16-byte aligned; vector stores
+ *        where ld_out is a multiple of 4.
+ *   out[m, n] = sum_b (xs[b, m] * w_s[n / 128, b]) * (sum_{k in b} xq[m, k] w[n, k])
+ *   rounded once to bf16; the scales' product and the sum over blocks in float,
+ *   the sum within a block by the matrix unit, whose accumulation keeps about
+ *   17 bits of that block's sum of |products|: below the output's 8.  The order
+ *   of the sum is fixed for given sizes and row strides.  Codes 0x7F and 0xFF
+ *   are NaN.
+ *   With the weight transposed (w as [K, N], w_s as [KB, NB]) the same calls
+ *   give the gradient with respect to the tokens: dx = dout . w.
+ *   K a multiple of 16, 16 <= K <= 2^20; 1 <= N <= 2^20; 0 <= M <= 4194303.
+ * ------------------------------------------------------------------------- */
+
+/* xs[b, t] = max(absmax of the block / 448, 2^-126), xq = E4M3 of x * (1 / xs),
+ * nearest, ties to even, in float.  A block that holds an infinity or a NaN
+ * gets the scale NaN and codes 0, so that the token's products are NaN.
+ *   x  bf16 bits [T, H], row stride ld_x (>= H, multiple of 8); H as K above.
+ *   xq uint8 [T, H]; xs float [ceil(H / 128), T], row stride ld_xs. */
+moe_status_t moe_quant_fp8(const uint16_t* x, int64_t ld_x, int T, int H, uint8_t* xq, float* xs,
+                           int64_t ld_xs, hipStream_t stream);
+
+/* Bytes of workspace for moe_fp8_linear (and so for moe_fp8_matmul) with these
+ * sizes: the product's partial sums, and the tokens in 8 bits with their
+ * scales.  It grows with M, so a buffer for M rows serves every smaller M with
+ * the same N and K.  0 for invalid sizes. */
+size_t moe_fp8_workspace_size(int M, int N, int K);
+
+/* Bytes of workspace for moe_fp8_matmul alone: the partial sums, at most
+ * 16 MB.  It grows with M.  0 where none is needed and for invalid sizes. */
+size_t moe_fp8_matmul_workspace_size(int M, int N, int K);
+
+moe_status_t moe_fp8_matmul(const uint8_t* xq, int64_t ld_xq, const float* xs, int64_t ld_xs,
+                            const uint8_t* w, const float* w_s, int M, int N, int K, uint16_t* out,
+                            int64_t ld_out, void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* moe_quant_fp8 of x [M, K] (bf16 bits, row stride ld_x, a multiple of 8) and
+ * moe_fp8_matmul as one call. */
+moe_status_t moe_fp8_linear(const uint16_t* x, int64_t ld_x, const uint8_t* w, const float* w_s,
+                            int M, int N, int K, uint16_t* out, int64_t ld_out, void* workspace,
+                            size_t ws_bytes, hipStream_t stream);
+
+/* Rows in expert order times their expert's weight: for expert e and output row
+ * j of [expert_offsets[e], expert_offsets[e + 1]),
+ *   out[j] = token(j) . w[e]^T,  token(j) = sorted_route[j] / top_k, or j itself
+ *   where sorted_route is NULL (tokens that stand in expert order already).
+ *   xq [rows, K], xs [KB, rows]; w [E_local, N, K], w_s [E_local, NB, KB];
+ *   expert_offsets int32 [E_local + 1] and sorted_route int32 [R] as moe_permute
+ *   gives them (read on the GPU: the call does not synchronise); out [R, N].
+ *   Output rows before the first offset and behind the last are left as they
+ *   were; offsets past R and routes past the tokens' rows are cut off there.
+ *   1 <= E_local <= 4096; 0 <= rows, R <= 2^30; without sorted_route rows >= R. */
+moe_status_t moe_fp8_grouped(const uint8_t* xq, int64_t ld_xq, const float* xs, int64_t ld_xs,
+                             int rows, const uint8_t* w, const float* w_s, int E_local, int N,
+                             int K, const int32_t* expert_offsets, const int32_t* sorted_route,
+                             int top_k, int R, uint16_t* out, int64_t ld_out,
+                             hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Tokens into expert order and back, and the gradients, for experts that run
+ * outside the five calls and for their training.  route_row int32 [T, top_k] as
+ * moe_permute gives it; a route whose row is negative or not below n_rows has
+ * no part.  Rows may have any length and stride and start at any element; sums
+ * in float, in slot order, one rounding; equal calls give equal bits.
+ * 1 <= H <= 2^20; 1 <= top_k <= 64; T * top_k <= 2^30; 0 <= n_rows <= 2^30
+ * (T * top_k serves every routing; fewer where the caller knows that no more
+ * routes are kept).
+ * ------------------------------------------------------------------------- */
+
+/* Element type of the rows (fixed values). */
+typedef enum moe_rows {
+  MOE_ROWS_BF16 = 0,
+  MOE_ROWS_F32 = 1
+} moe_rows_t;
+
+/* rows[route_row[t, k]] = x[t] for every kept route; other rows are left as
+ * they were.  Its gradient is moe_unsort_tokens without weights.
+ *   x [T, H], row stride ld_x; rows [n_rows, H], row stride ld_rows; no overlap. */
+moe_status_t moe_sort_tokens(const void* x, int64_t ld_x, int T, int H, int top_k,
+                             const int32_t* route_row, int type, void* rows, int64_t ld_rows,
+                             int n_rows, hipStream_t stream);
+
+/* out[t] = sum over kept k of topk_w[t, k] * rows[route_row[t, k]]; with topk_w
+ * NULL the plain sum.  A token with no kept route gets zeros.
+ *   rows [n_rows, H], row stride ld_rows; topk_w float [T, top_k]; out [T, H],
+ *   row stride ld_out; no overlap. */
+moe_status_t moe_unsort_tokens(const void* rows, int64_t ld_rows, int n_rows, int T, int H,
+                               int top_k, const int32_t* route_row, const float* topk_w, int type,
+                               void* out, int64_t ld_out, hipStream_t stream);
+
+/* Gradients of the weighted moe_unsort_tokens:
+ *   drows[route_row[t, k]] = topk_w[t, k] * dout[t] (other rows left as they were),
+ *   dw[t, k] = sum_h dout[t, h] * rows[route_row[t, k], h] in float (0 for a
+ *   route that is not kept).
+ *   drows [n_rows, H], row stride ld_drows, or NULL for none; dw float [T,
+ *   top_k], or NULL for none (rows is not read then); at least one of the two. */
+moe_status_t moe_unsort_tokens_grad(const void* dout, int64_t ld_dout, const void* rows,
+                                    int64_t ld_rows, int n_rows, int T, int H, int top_k,
+                                    const int32_t* route_row, const float* topk_w, int type,
+                                    void* drows, int64_t ld_drows, float* dw, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

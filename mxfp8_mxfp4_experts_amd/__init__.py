@@ -9,6 +9,10 @@ given top-k ids, quantisation and grouping as ``moe_quant_permute``).
 Around the experts there are the residual's norm with an 8-bit output, the
 router's product, group-limited routing and dense projections in 8-bit
 integers; ``MoEBlock`` runs them with a ``MoELayer`` as one MoE block.
+
+Beside these there are products in E4M3 with a float scale per block of 128
+(dense, and grouped by expert), and the way of tokens into expert order and
+back with its gradients.
 """
 from ._binding import (  # noqa: F401
     COMBINE_ATOMIC,
@@ -28,6 +32,11 @@ from ._binding import (  # noqa: F401
     moe_add_rmsnorm,
     moe_fc1_situ,
     moe_fc2_combine,
+    moe_fp8_grouped,
+    moe_fp8_linear,
+    moe_fp8_matmul,
+    moe_fp8_matmul_workspace_size,
+    moe_fp8_workspace_size,
     moe_gate_logits,
     moe_gate_workspace_size,
     moe_int8_linear,
@@ -42,12 +51,16 @@ from ._binding import (  # noqa: F401
     moe_prepack_w13,
     moe_prepack_w13_layout,
     moe_prepack_w2,
+    moe_quant_fp8,
     moe_quant_int8,
     moe_quant_mxfp8,
     moe_quant_permute,
     moe_route,
     moe_route_groups,
     moe_route_quant_permute,
+    moe_sort_tokens,
+    moe_unsort_tokens,
+    moe_unsort_tokens_grad,
     moe_workspace_size,
 )
 from .block import MoEBlock  # noqa: F401

@@ -32,6 +32,9 @@ EXPORTS = (
     "moe_add_rmsnorm", "moe_quant_int8", "moe_int8_workspace_size",
     "moe_int8_matmul_workspace_size", "moe_int8_matmul", "moe_int8_linear",
     "moe_gate_workspace_size", "moe_gate_logits", "moe_route_groups",
+    "moe_quant_fp8", "moe_fp8_workspace_size", "moe_fp8_matmul_workspace_size", "moe_fp8_matmul",
+    "moe_fp8_linear", "moe_fp8_grouped", "moe_sort_tokens", "moe_unsort_tokens",
+    "moe_unsort_tokens_grad",
 )
 
 # moe_w13_layout_t values (row order of a w13 tensor)
@@ -45,6 +48,8 @@ _OUT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
 # moe_score_t and moe_group_score_t values (moe_route_groups)
 SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
 GROUP_MAX, GROUP_TOP2 = 0, 1
+# moe_rows_t values, by dtype of the rows that are sorted by expert
+_ROW_TYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -111,6 +116,25 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.moe_gate_logits.argtypes = [_P, _I64, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]
     lib.moe_route_groups.restype = _I
     lib.moe_route_groups.argtypes = [_P, _I64, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P]
+    lib.moe_quant_fp8.restype = _I
+    lib.moe_quant_fp8.argtypes = [_P, _I64, _I, _I, _P, _P, _I64, _P]
+    for name in ("moe_fp8_workspace_size", "moe_fp8_matmul_workspace_size"):
+        getattr(lib, name).restype = _SZ
+        getattr(lib, name).argtypes = [_I, _I, _I]
+    lib.moe_fp8_matmul.restype = _I
+    lib.moe_fp8_matmul.argtypes = [_P, _I64, _P, _I64, _P, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]
+    lib.moe_fp8_linear.restype = _I
+    lib.moe_fp8_linear.argtypes = [_P, _I64, _P, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]
+    lib.moe_fp8_grouped.restype = _I
+    lib.moe_fp8_grouped.argtypes = [_P, _I64, _P, _I64, _I, _P, _P, _I, _I, _I, _P, _P, _I, _I, _P,
+                                    _I64, _P]
+    lib.moe_sort_tokens.restype = _I
+    lib.moe_sort_tokens.argtypes = [_P, _I64, _I, _I, _I, _P, _I, _P, _I64, _I, _P]
+    lib.moe_unsort_tokens.restype = _I
+    lib.moe_unsort_tokens.argtypes = [_P, _I64, _I, _I, _I, _I, _P, _P, _I, _P, _I64, _P]
+    lib.moe_unsort_tokens_grad.restype = _I
+    lib.moe_unsort_tokens_grad.argtypes = [_P, _I64, _P, _I64, _I, _I, _I, _I, _P, _P, _I, _P,
+                                           _I64, _P, _P]
     return lib
 
 
@@ -784,3 +808,304 @@ def moe_route_groups(logits, bias, top_k: int, n_group: int = 1, topk_group: int
     if st:
         raise MoEError("moe_route_groups", st)
     return topk_idx, topk_w
+
+
+# ---------------------------------------------------------------------------
+# Products in E4M3 with a float scale for each block of 128.  Codes are uint8 or
+# torch.float8_e4m3fn tensors.
+
+_FP8 = torch.float8_e4m3fn
+
+
+def _codes(t, name, rows, cols, idx):
+    """Address and row stride of E4M3 codes [rows, cols] whose rows may be strided."""
+    p = _plain(t, _U8, rows, cols, idx)
+    if p < 0:
+        p = _plain(t, _FP8, rows, cols, idx)
+    if p >= 0:
+        return p, cols
+    return _rows(t, name, _FP8 if isinstance(t, torch.Tensor) and t.dtype == _FP8 else _U8, rows,
+                 cols, idx)
+
+
+def _scales(xs, K, rows, idx):
+    """Address and row stride of the tokens' scales, [ceil(K / 128), rows]."""
+    KB = (K + 127) // 128
+    p = _plain(xs, _F32, KB, rows, idx)
+    return (p, rows) if p >= 0 else _rows(xs, "xs", _F32, KB, rows, idx)
+
+
+def _fp8_weight(w, w_s, K, idx):
+    """N and the addresses of a weight's codes [N, K] and scales [NB, KB]."""
+    N = w.shape[0] if isinstance(w, torch.Tensor) and w.dim() == 2 else -1
+    if N < 0 or w.shape[1] != K:
+        raise ValueError(f"w must be [N, {K}]")
+    w_p = _plain(w, _FP8, N, K, idx)
+    if w_p < 0:
+        w_p = _plain(w, _U8, N, K, idx)
+    if w_p < 0:
+        _refuse(w, "w", _FP8 if w.dtype == _FP8 else _U8, (N, K), idx)
+    NB, KB = (N + 127) // 128, (K + 127) // 128
+    s_p = _plain(w_s, _F32, NB, KB, idx)
+    if s_p < 0:
+        _refuse(w_s, "w_s", _F32, (NB, KB), idx)
+    return N, w_p, s_p
+
+
+def _bf16_out(out, rows, cols, idx):
+    if out is None:
+        out = _new((rows, cols), _BF16, idx)
+    p, ld = _plain(out, _BF16, rows, cols, idx), cols
+    if p < 0:
+        p, ld = _rows(out, "out", _BF16, rows, cols, idx)
+    return out, p, ld
+
+
+def moe_quant_fp8(x, xq=None, xs=None):
+    """bf16 rows [T, H] -> E4M3 codes uint8 [T, H] and float scales
+    [ceil(H / 128), T], one for each row and 128 elements."""
+    head = _head(x)
+    if head is None:
+        _no_head(x, "x")
+    idx, T, H = head
+    x_p, ld_x = _plain(x, _BF16, T, H, idx), H
+    if x_p < 0:
+        x_p, ld_x = _rows(x, "x", _BF16, T, H, idx)
+    if xq is None:
+        xq = _new((T, H), _U8, idx)
+    q_p = _plain(xq, _U8, T, H, idx)
+    if q_p < 0:
+        q_p = _plain(xq, _FP8, T, H, idx)
+    if q_p < 0:
+        _refuse(xq, "xq", _U8, (T, H), idx)
+    if xs is None:
+        xs = _new(((H + 127) // 128, T), _F32, idx)
+    s_p, ld_s = _scales(xs, H, T, idx)
+    st = (_lib or lib()).moe_quant_fp8(x_p, ld_x, T, H, q_p, s_p, ld_s, _raw_stream(idx))
+    if st:
+        raise MoEError("moe_quant_fp8", st)
+    return xq, xs
+
+
+def moe_fp8_workspace_size(M: int, N: int, K: int) -> int:
+    """Workspace bytes of moe_fp8_linear and moe_fp8_matmul; a buffer for M rows
+    serves fewer."""
+    n = lib().moe_fp8_workspace_size(M, N, K)
+    if n == 0:
+        raise ValueError("invalid sizes for moe_fp8_workspace_size")
+    return n
+
+
+def moe_fp8_matmul_workspace_size(M: int, N: int, K: int) -> int:
+    """Workspace bytes of moe_fp8_matmul alone; a buffer for M rows serves
+    fewer."""
+    return lib().moe_fp8_matmul_workspace_size(M, N, K)
+
+
+def moe_fp8_matmul(xq, xs, w, w_s, out=None, workspace=None):
+    """out bf16 [M, N] = xq [M, K] . w [N, K], both E4M3, scaled block by block:
+    xs float [ceil(K / 128), M], w_s float [ceil(N / 128), ceil(K / 128)]."""
+    head = _head(xq)
+    if head is None:
+        _no_head(xq, "xq")
+    idx, M, K = head
+    q_p, ld_xq = _codes(xq, "xq", M, K, idx)
+    x_p, ld_xs = _scales(xs, K, M, idx)
+    N, w_p, s_p = _fp8_weight(w, w_s, K, idx)
+    out, o_p, ld_out = _bf16_out(out, M, N, idx)
+    L = _lib or lib()
+    workspace = _workspace(workspace, L.moe_fp8_matmul_workspace_size, (M, N, K), idx)
+    st = L.moe_fp8_matmul(q_p, ld_xq, x_p, ld_xs, w_p, s_p, M, N, K, o_p, ld_out,
+                          workspace.data_ptr(), workspace.numel(), _raw_stream(idx))
+    if st:
+        raise MoEError("moe_fp8_matmul", st)
+    return out
+
+
+def moe_fp8_linear(x, w, w_s, out=None, workspace=None):
+    """moe_quant_fp8 of x [M, K] (bf16) and moe_fp8_matmul as one call."""
+    head = _head(x)
+    if head is None:
+        _no_head(x, "x")
+    idx, M, K = head
+    x_p, ld_x = _plain(x, _BF16, M, K, idx), K
+    if x_p < 0:
+        x_p, ld_x = _rows(x, "x", _BF16, M, K, idx)
+    N, w_p, s_p = _fp8_weight(w, w_s, K, idx)
+    out, o_p, ld_out = _bf16_out(out, M, N, idx)
+    L = _lib or lib()
+    workspace = _workspace(workspace, L.moe_fp8_workspace_size, (M, N, K), idx)
+    st = L.moe_fp8_linear(x_p, ld_x, w_p, s_p, M, N, K, o_p, ld_out, workspace.data_ptr(),
+                          workspace.numel(), _raw_stream(idx))
+    if st:
+        raise MoEError("moe_fp8_linear", st)
+    return out
+
+
+def moe_fp8_grouped(xq, xs, w, w_s, expert_offsets, sorted_route=None, top_k: int = 1, out=None):
+    """Rows [expert_offsets[e], expert_offsets[e + 1]) of ``out`` bf16 [R, N] =
+    their tokens times w[e]: w E4M3 [E, N, K], w_s float [E, ceil(N / 128),
+    ceil(K / 128)].  With ``sorted_route`` int32 [R] (moe_permute) row j's token
+    is xq[sorted_route[j] / top_k], without it xq stands in expert order.  Rows
+    behind the last expert's are left as they were (a new ``out`` holds anything
+    there)."""
+    head = _head(xq)
+    if head is None:
+        _no_head(xq, "xq")
+    idx, rows, K = head
+    q_p, ld_xq = _codes(xq, "xq", rows, K, idx)
+    x_p, ld_xs = _scales(xs, K, rows, idx)
+    if not isinstance(w, torch.Tensor) or w.dim() != 3 or w.shape[2] != K:
+        raise ValueError(f"w must be [E, N, {K}]")
+    E, N, _ = w.shape
+    if w.dtype is not _FP8 and w.dtype is not _U8:
+        raise ValueError(f"w must be uint8 or float8_e4m3fn, got {w.dtype}")
+    if w.get_device() != idx or not w.is_contiguous():
+        raise ValueError(f"w must be contiguous and on cuda:{idx}")
+    s_shape = (E, (N + 127) // 128, (K + 127) // 128)
+    if not isinstance(w_s, torch.Tensor) or w_s.dtype is not _F32 or w_s.shape != s_shape:
+        raise ValueError(f"w_s must be torch.float32 {s_shape}")
+    if w_s.get_device() != idx or not w_s.is_contiguous():
+        raise ValueError(f"w_s must be contiguous and on cuda:{idx}")
+    o_p = _plain(expert_offsets, _I32, E + 1, -1, idx)
+    if o_p < 0:
+        _refuse(expert_offsets, "expert_offsets", _I32, (E + 1,), idx)
+    r_p = None
+    if sorted_route is not None:
+        R = sorted_route.numel() if isinstance(sorted_route, torch.Tensor) else -1
+        r_p = _plain(sorted_route, _I32, R, -1, idx)
+        if r_p < 0:
+            _refuse(sorted_route, "sorted_route", _I32, (R,), idx)
+    else:
+        R = rows
+    out, out_p, ld_out = _bf16_out(out, R, N, idx)
+    st = (_lib or lib()).moe_fp8_grouped(q_p, ld_xq, x_p, ld_xs, rows, w.data_ptr(),
+                                         w_s.data_ptr(), E, N, K, o_p, r_p, top_k, R, out_p,
+                                         ld_out, _raw_stream(idx))
+    if st:
+        raise MoEError("moe_fp8_grouped", st)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Tokens into expert order and back.
+
+def _row_type(t, name):
+    kind = _ROW_TYPE.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return kind
+
+
+def _any_rows(t, name, dtype, rows, cols, idx):
+    """Address and row stride, contiguous or not."""
+    p = _plain(t, dtype, rows, cols, idx)
+    return (p, cols) if p >= 0 else _rows(t, name, dtype, rows, cols, idx)
+
+
+def _routes(route_row, T, top_k, idx):
+    p = _plain(route_row, _I32, T * top_k, -1, idx)
+    if p < 0:
+        p = _plain(route_row, _I32, T, top_k, idx)
+    if p < 0:
+        _refuse(route_row, "route_row", _I32, (T * top_k,), idx)
+    return p
+
+
+def _tokens_of(route_row, top_k):
+    if not isinstance(route_row, torch.Tensor):
+        raise ValueError("route_row must be a torch.Tensor")
+    if top_k < 1 or route_row.numel() % top_k:
+        raise ValueError(f"route_row must hold top_k = {top_k} routes for every token")
+    return route_row.numel() // top_k
+
+
+def moe_sort_tokens(x, route_row, top_k: int, rows=None):
+    """rows[route_row[t, k]] = x[t] for every kept route: x [T, H] bf16 or
+    float32, route_row int32 [T * top_k] of moe_permute, rows [n, H] (n = T *
+    top_k where not given, and rows that no route has hold anything then).  Its
+    gradient is ``moe_unsort_tokens(drows, route_row, None, top_k)``."""
+    head = _head(x)
+    if head is None:
+        _no_head(x, "x")
+    idx, T, H = head
+    kind = _row_type(x, "x")
+    x_p, ld_x = _any_rows(x, "x", x.dtype, T, H, idx)
+    r_p = _routes(route_row, T, top_k, idx)
+    if rows is None:
+        rows = _new((T * top_k, H), x.dtype, idx)
+    n = rows.shape[0] if isinstance(rows, torch.Tensor) and rows.dim() == 2 else -1
+    o_p, ld = _any_rows(rows, "rows", x.dtype, n, H, idx)
+    st = (_lib or lib()).moe_sort_tokens(x_p, ld_x, T, H, top_k, r_p, kind, o_p, ld, n,
+                                         _raw_stream(idx))
+    if st:
+        raise MoEError("moe_sort_tokens", st)
+    return rows
+
+
+def moe_unsort_tokens(rows, route_row, topk_w, top_k: int, out=None):
+    """out[t] = sum over kept k of topk_w[t, k] * rows[route_row[t, k]]: rows
+    [n, H] bf16 or float32, topk_w float [T, top_k] or None (the plain sum),
+    out [T, H] of the rows' type."""
+    head = _head(rows)
+    if head is None:
+        _no_head(rows, "rows")
+    idx, n, H = head
+    kind = _row_type(rows, "rows")
+    T = _tokens_of(route_row, top_k)
+    r_p = _routes(route_row, T, top_k, idx)
+    in_p, ld = _any_rows(rows, "rows", rows.dtype, n, H, idx)
+    w_p = None
+    if topk_w is not None:
+        w_p = _plain(topk_w, _F32, T, top_k, idx)
+        if w_p < 0:
+            _refuse(topk_w, "topk_w", _F32, (T, top_k), idx)
+    if out is None:
+        out = _new((T, H), rows.dtype, idx)
+    o_p, ld_out = _any_rows(out, "out", rows.dtype, T, H, idx)
+    st = (_lib or lib()).moe_unsort_tokens(in_p, ld, n, T, H, top_k, r_p, w_p, kind, o_p, ld_out,
+                                           _raw_stream(idx))
+    if st:
+        raise MoEError("moe_unsort_tokens", st)
+    return out
+
+
+def moe_unsort_tokens_grad(dout, rows, route_row, topk_w, drows=None, dw=None,
+                           want_drows: bool = True, want_dw: bool = True):
+    """Gradients of the weighted ``moe_unsort_tokens``: ``(drows, dw)`` with
+    drows[route_row[t, k]] = topk_w[t, k] * dout[t] (other rows are left as they
+    were; a new ``drows`` holds anything there) and dw float [T, top_k], dw[t, k]
+    = <dout[t], rows[route_row[t, k]]>.  ``want_drows`` / ``want_dw`` False
+    leaves one out (None) where no buffer is given."""
+    head = _head(dout)
+    if head is None:
+        _no_head(dout, "dout")
+    idx, T, H = head
+    kind = _row_type(dout, "dout")
+    d_p, ld_d = _any_rows(dout, "dout", dout.dtype, T, H, idx)
+    if not isinstance(topk_w, torch.Tensor) or topk_w.dim() != 2:
+        raise ValueError(f"topk_w must be [{T}, top_k]")
+    top_k = topk_w.shape[1]
+    w_p = _plain(topk_w, _F32, T, top_k, idx)
+    if w_p < 0:
+        _refuse(topk_w, "topk_w", _F32, (T, top_k), idx)
+    r_p = _routes(route_row, T, top_k, idx)
+    n = rows.shape[0] if isinstance(rows, torch.Tensor) and rows.dim() == 2 else -1
+    in_p, ld = _any_rows(rows, "rows", dout.dtype, n, H, idx)
+    if drows is None and want_drows:
+        drows = _new((n, H), dout.dtype, idx)
+    o_p, ld_o = None, H
+    if drows is not None:
+        o_p, ld_o = _any_rows(drows, "drows", dout.dtype, n, H, idx)
+    if dw is None and want_dw:
+        dw = _new((T, top_k), _F32, idx)
+    dw_p = None
+    if dw is not None:
+        dw_p = _plain(dw, _F32, T, top_k, idx)
+        if dw_p < 0:
+            _refuse(dw, "dw", _F32, (T, top_k), idx)
+    st = (_lib or lib()).moe_unsort_tokens_grad(d_p, ld_d, in_p, ld, n, T, H, top_k, r_p, w_p,
+                                                kind, o_p, ld_o, dw_p, _raw_stream(idx))
+    if st:
+        raise MoEError("moe_unsort_tokens_grad", st)
+    return drows, dw

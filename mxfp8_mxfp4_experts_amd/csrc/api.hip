@@ -69,6 +69,43 @@ bool valid_gate(int T, int E, int H) {
          H % 8 == 0;
 }
 
+bool valid_fp8(int M, int N, int K) {
+  return M >= 0 && M <= kMaxRows && N >= 1 && N <= kMaxFp8K && K >= 16 && K <= kMaxFp8K &&
+         K % 16 == 0;
+}
+
+// Workspace of moe_fp8_linear: partial sums of the product at its start, then
+// the tokens in 8 bits, in rows of whole 128-byte lines, and their scales.
+struct Fp8Layout {
+  size_t xq, xs, total;
+  int64_t ld_q, ld_s;
+};
+Fp8Layout fp8_layout(int M, int N, int K) {
+  Fp8Layout l;
+  const int64_t blocks = ((int64_t)K + 127) / 128;
+  l.xq = align256(fp8_workspace(M, N));
+  l.ld_q = blocks * 128;
+  l.ld_s = ((int64_t)M + 3) / 4 * 4;
+  l.xs = align256(l.xq + (size_t)M * l.ld_q);
+  l.total = align256(l.xs + sizeof(float) * (size_t)(blocks * l.ld_s) + 1);
+  return l;
+}
+
+Fp8Params fp8_params(const uint8_t* xq, int64_t ld_xq, const float* xs, int64_t ld_xs, int rows,
+                     const uint8_t* w, const float* w_s, int M, int N, int K, uint16_t* out,
+                     int64_t ld_out, void* workspace) {
+  return Fp8Params{xq, ld_xq, xs, ld_xs, w, w_s, M, N, K, out, ld_out, ld_out % 4 == 0, workspace,
+                   1, nullptr, nullptr, 1, rows};
+}
+
+// Tokens into expert order and back.
+bool valid_sort(int T, int H, int top_k, int n_rows) {
+  return T >= 0 && H >= 1 && H <= kMaxSortH && top_k >= 1 && top_k <= kMaxTopK &&
+         (int64_t)T * top_k <= kMaxRoutes && n_rows >= 0 && n_rows <= kMaxRoutes;
+}
+bool valid_row_type(int type) { return type == MOE_ROWS_BF16 || type == MOE_ROWS_F32; }
+size_t row_align(int type) { return type == MOE_ROWS_F32 ? 4 : 2; }
+
 // Workspace of moe_int8_linear: partial sums of the product at its start,
 // then the tokens in 8 bits, in rows of whole 128-byte lines, and their scales.
 struct Int8Layout {
@@ -550,6 +587,176 @@ moe_status_t moe_route_groups(const float* logits, int64_t ld_logits, const floa
   const RouteGroupsParams p{logits, ld_logits, bias, T, E, top_k, n_group, topk_group, score,
                             group_score, renormalise != 0, routed_scaling, topk_idx, topk_w};
   return finish(launch_route_groups(p, stream));
+}
+
+moe_status_t moe_quant_fp8(const uint16_t* x, int64_t ld_x, int T, int H, uint8_t* xq, float* xs,
+                           int64_t ld_xs, hipStream_t stream) {
+  if (!valid_fp8(T, 1, H) || ld_x < H || ld_xs < T) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!x || !xq || !xs) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(xq, 16) || !aligned(xs, 4))
+    return MOE_ERR_ALIGN;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  return finish(launch_quant_fp8(x, ld_x, T, H, xq, H, xs, ld_xs, stream));
+}
+
+size_t moe_fp8_workspace_size(int M, int N, int K) {
+  if (!valid_fp8(M, N, K)) return 0;
+  return fp8_layout(M, N, K).total;
+}
+
+size_t moe_fp8_matmul_workspace_size(int M, int N, int K) {
+  if (!valid_fp8(M, N, K)) return 0;
+  return fp8_layout(M, N, K).xq;
+}
+
+moe_status_t moe_fp8_matmul(const uint8_t* xq, int64_t ld_xq, const float* xs, int64_t ld_xs,
+                            const uint8_t* w, const float* w_s, int M, int N, int K, uint16_t* out,
+                            int64_t ld_out, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  if (!valid_fp8(M, N, K) || ld_xq < K || ld_xs < M || ld_out < N) return MOE_ERR_SHAPE;
+  if (M == 0) return MOE_OK;
+  const Fp8Layout l = fp8_layout(M, N, K);
+  if (!xq || !xs || !w || !w_s || !out || (!workspace && l.xq > 0)) return MOE_ERR_NULL;
+  if (!aligned(xq, 16) || ld_xq % 16 != 0 || !aligned(xs, 4) || !aligned(w, 16) ||
+      !aligned(w_s, 4) || !aligned(out, 16) || !aligned(workspace, 256))
+    return MOE_ERR_ALIGN;
+  if (ws_bytes < l.xq) return MOE_ERR_WORKSPACE;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  return finish(launch_fp8(
+      fp8_params(xq, ld_xq, xs, ld_xs, M, w, w_s, M, N, K, out, ld_out, workspace), stream));
+}
+
+moe_status_t moe_fp8_linear(const uint16_t* x, int64_t ld_x, const uint8_t* w, const float* w_s,
+                            int M, int N, int K, uint16_t* out, int64_t ld_out, void* workspace,
+                            size_t ws_bytes, hipStream_t stream) {
+  if (!valid_fp8(M, N, K) || ld_x < K || ld_out < N) return MOE_ERR_SHAPE;
+  if (M == 0) return MOE_OK;
+  if (!x || !w || !w_s || !out || !workspace) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(w, 16) || !aligned(w_s, 4) ||
+      !aligned(out, 16) || !aligned(workspace, 256))
+    return MOE_ERR_ALIGN;
+  const Fp8Layout l = fp8_layout(M, N, K);
+  if (ws_bytes < l.total) return MOE_ERR_WORKSPACE;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  uint8_t* xq = static_cast<uint8_t*>(workspace) + l.xq;
+  float* xs = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.xs);
+  if (launch_quant_fp8(x, ld_x, M, K, xq, l.ld_q, xs, l.ld_s, stream) != hipSuccess)
+    return MOE_ERR_HIP;
+  return finish(launch_fp8(
+      fp8_params(xq, l.ld_q, xs, l.ld_s, M, w, w_s, M, N, K, out, ld_out, workspace), stream));
+}
+
+moe_status_t moe_fp8_grouped(const uint8_t* xq, int64_t ld_xq, const float* xs, int64_t ld_xs,
+                             int rows, const uint8_t* w, const float* w_s, int E_local, int N,
+                             int K, const int32_t* expert_offsets, const int32_t* sorted_route,
+                             int top_k, int R, uint16_t* out, int64_t ld_out,
+                             hipStream_t stream) {
+  if (rows < 0 || rows > kMaxRoutes || !valid_fp8(0, N, K) || E_local < 1 ||
+      E_local > kMaxExperts || ld_xq < K || ld_xs < rows || ld_out < N || R < 0 ||
+      R > kMaxRoutes || top_k < 1 || top_k > kMaxTopK || (!sorted_route && rows < R))
+    return MOE_ERR_SHAPE;
+  if (R == 0 || rows == 0) return MOE_OK;
+  if (!xq || !xs || !w || !w_s || !expert_offsets || !out) return MOE_ERR_NULL;
+  if (!aligned(xq, 16) || ld_xq % 16 != 0 || !aligned(xs, 4) || !aligned(w, 16) ||
+      !aligned(w_s, 4) || !aligned(out, 16) || !aligned(expert_offsets, 4) ||
+      !aligned(sorted_route, 4))
+    return MOE_ERR_ALIGN;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  Fp8Params p = fp8_params(xq, ld_xq, xs, ld_xs, rows, w, w_s, R, N, K, out, ld_out, nullptr);
+  p.E = E_local;
+  p.offs = expert_offsets;
+  p.route = sorted_route;
+  p.top_k = top_k;
+  return finish(launch_fp8(p, stream));
+}
+
+moe_status_t moe_sort_tokens(const void* x, int64_t ld_x, int T, int H, int top_k,
+                             const int32_t* route_row, int type, void* rows, int64_t ld_rows,
+                             int n_rows, hipStream_t stream) {
+  if (!valid_row_type(type)) return MOE_ERR_ENUM;
+  if (!valid_sort(T, H, top_k, n_rows) || ld_x < H || ld_rows < H) return MOE_ERR_SHAPE;
+  if (T == 0 || n_rows == 0) return MOE_OK;
+  if (!x || !route_row || !rows) return MOE_ERR_NULL;
+  if (!aligned(x, row_align(type)) || !aligned(rows, row_align(type)) || !aligned(route_row, 4))
+    return MOE_ERR_ALIGN;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  SortParams p{};
+  p.x = const_cast<void*>(x);
+  p.ld_x = ld_x;
+  p.T = T;
+  p.H = H;
+  p.top_k = top_k;
+  p.route_row = route_row;
+  p.rows = rows;
+  p.ld_rows = ld_rows;
+  p.n_rows = n_rows;
+  return finish(launch_sort(p, SortOp::kSort, type == MOE_ROWS_F32, stream));
+}
+
+moe_status_t moe_unsort_tokens(const void* rows, int64_t ld_rows, int n_rows, int T, int H,
+                               int top_k, const int32_t* route_row, const float* topk_w, int type,
+                               void* out, int64_t ld_out, hipStream_t stream) {
+  if (!valid_row_type(type)) return MOE_ERR_ENUM;
+  if (!valid_sort(T, H, top_k, n_rows) || ld_rows < H || ld_out < H) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if ((!rows && n_rows > 0) || !route_row || !out) return MOE_ERR_NULL;
+  if (!aligned(rows, row_align(type)) || !aligned(out, row_align(type)) ||
+      !aligned(route_row, 4) || !aligned(topk_w, 4))
+    return MOE_ERR_ALIGN;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  SortParams p{};
+  p.x = out;
+  p.ld_x = ld_out;
+  p.T = T;
+  p.H = H;
+  p.top_k = top_k;
+  p.route_row = route_row;
+  p.rows = const_cast<void*>(rows);
+  p.ld_rows = ld_rows;
+  p.n_rows = n_rows;
+  p.w = topk_w;
+  return finish(launch_sort(p, SortOp::kUnsort, type == MOE_ROWS_F32, stream));
+}
+
+moe_status_t moe_unsort_tokens_grad(const void* dout, int64_t ld_dout, const void* rows,
+                                    int64_t ld_rows, int n_rows, int T, int H, int top_k,
+                                    const int32_t* route_row, const float* topk_w, int type,
+                                    void* drows, int64_t ld_drows, float* dw,
+                                    hipStream_t stream) {
+  if (!valid_row_type(type)) return MOE_ERR_ENUM;
+  if (!valid_sort(T, H, top_k, n_rows) || ld_dout < H || (dw && ld_rows < H) ||
+      (drows && ld_drows < H))
+    return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!dout || !route_row || !topk_w || (!drows && !dw) || (dw && !rows && n_rows > 0))
+    return MOE_ERR_NULL;
+  const size_t a = row_align(type);
+  if (!aligned(dout, a) || !aligned(rows, a) || !aligned(drows, a) || !aligned(route_row, 4) ||
+      !aligned(topk_w, 4) || !aligned(dw, 4))
+    return MOE_ERR_ALIGN;
+  moe_status_t s = check_device();
+  if (s != MOE_OK) return s;
+  SortParams p{};
+  p.T = T;
+  p.H = H;
+  p.top_k = top_k;
+  p.route_row = route_row;
+  p.rows = const_cast<void*>(rows);
+  p.ld_rows = ld_rows;
+  p.n_rows = n_rows;
+  p.w = topk_w;
+  p.dout = dout;
+  p.ld_dout = ld_dout;
+  p.drows = drows;
+  p.ld_drows = ld_drows;
+  p.dw = dw;
+  return finish(launch_sort(p, SortOp::kGrad, type == MOE_ROWS_F32, stream));
 }
 
 }  // extern "C"

@@ -17,6 +17,9 @@ constexpr int kMaxNormH = 32768;    // row width of the norm (1024 threads, 32 e
 constexpr int kMaxInt8K = 131056;   // 128 * 128 * K < 2^31
 constexpr int kMaxInt8N = 1 << 20;
 constexpr int kMaxGateH = 1 << 20;
+constexpr int kMaxFp8K = 1 << 20;   // and N
+constexpr int kMaxSortH = 1 << 20;
+constexpr int kMaxRoutes = 1 << 30;
 constexpr int kGroup = 32;          // MX block: one E8M0 scale per 32 elements
 
 // FC tile heights (token rows per workgroup tile) for which moe_permute

@@ -127,4 +127,48 @@ hipError_t launch_dense_quant(int q, const DenseParams& p, const uint16_t* x,
                               int64_t ld_x, hipStream_t stream);
 hipError_t launch_dense(bool i8, const DenseParams& p, hipStream_t stream);
 
+// Block-scaled FP8 products (fp8.hip).
+struct Fp8Params {
+  const uint8_t* a;         // tokens [a_rows, K], row stride ld_a
+  int64_t ld_a;
+  const float* sa;          // their scales [K / 128][a_rows], row stride ld_sa
+  int64_t ld_sa;
+  const uint8_t* b;         // weights [N, K] or [E, N, K]
+  const float* sb;          // their scales [N / 128, K / 128] or [E, ...]
+  int M, N, K;              // M: rows of out
+  uint16_t* out;
+  int64_t ld_out;
+  int out_vec;              // rows take 4-element vector stores
+  void* partial;            // dense: fp8_workspace bytes
+  // Grouped (offs null: dense).
+  int E;
+  const int32_t* offs;      // [E + 1]
+  const int32_t* route;     // [M] or null: output row's token is route / top_k
+  int top_k;
+  int a_rows;
+};
+size_t fp8_workspace(int M, int N);   // grows with M
+hipError_t launch_quant_fp8(const uint16_t* x, int64_t ld_x, int T, int H, uint8_t* xq,
+                            int64_t ld_q, float* xs, int64_t ld_s, hipStream_t stream);
+hipError_t launch_fp8(const Fp8Params& p, hipStream_t stream);
+
+// Tokens into expert order and back (sort.hip).
+enum class SortOp { kSort, kUnsort, kGrad };
+struct SortParams {
+  void* x;                  // sort: x; unsort: out; [T, H]
+  int64_t ld_x;
+  int T, H, top_k;
+  const int32_t* route_row; // [T, top_k]
+  void* rows;               // [n_rows, H]
+  int64_t ld_rows;
+  int n_rows;
+  const float* w;           // [T, top_k]; unsort: or null
+  const void* dout;         // grad: [T, H]
+  int64_t ld_dout;
+  void* drows;              // grad: or null
+  int64_t ld_drows;
+  float* dw;                // grad: or null
+};
+hipError_t launch_sort(const SortParams& p, SortOp op, bool f32, hipStream_t stream);
+
 }  // namespace mi355moe

@@ -1,0 +1,251 @@
+// Tokens into expert order and back, and the gradients of both ways.
+//
+//   sort     rows[route_row[t, k]] = x[t]
+//   unsort   out[t] = sum over kept k of w[t, k] rows[route_row[t, k]] (or without w, which is
+//            also the sort's gradient), in k order, float sums, one rounding
+//   grad     of the weighted unsort: drows[route_row[t, k]] = w[t, k] dout[t] and
+//            dw[t, k] = <dout[t], rows[route_row[t, k]]> (float)
+//
+// All three run token by token, so that what a token's routes share (x[t], out[t], dout[t]) is
+// read or written once and what they differ in moves as whole rows; nothing is added with
+// atomics, and equal calls give equal bits.  Memory bounds them at many tokens.
+//
+// A row is cut into pieces of 16 bytes.  Rows may start at any element and have any length: the
+// pieces are accessed at element alignment (gfx950 takes that), and a row's last piece is moved
+// back to end with the row, where it repeats elements of the piece before it (the same values
+// stored twice; a sum counts them once).  Rows shorter than a piece go element by element.
+#include "common.h"
+#include "launch.h"
+#include "q8_dev.h"
+
+namespace mi355moe {
+
+namespace {
+
+// V elements of type T as floats, and the raw piece they are loaded as.
+template <class T, int V>
+struct Piece;
+template <>
+struct Piece<uint16_t, 8> {
+  typedef uint32_t Raw __attribute__((ext_vector_type(4), aligned(2)));
+  static __device__ __forceinline__ void floats(Raw v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_to_f32(v[i] & 0xFFFFu);
+      f[2 * i + 1] = bf16_to_f32(v[i] >> 16);
+    }
+  }
+  static __device__ __forceinline__ Raw raw(const float (&f)[8]) {
+    return Raw{f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]),
+               f32x2_to_bf16x2(f[4], f[5]), f32x2_to_bf16x2(f[6], f[7])};
+  }
+};
+template <>
+struct Piece<uint16_t, 1> {
+  typedef uint16_t Raw;
+  static __device__ __forceinline__ void floats(Raw v, float (&f)[1]) { f[0] = bf16_to_f32(v); }
+  static __device__ __forceinline__ Raw raw(const float (&f)[1]) {
+    return (Raw)f32x2_to_bf16x2(f[0], 0.0f);
+  }
+};
+template <>
+struct Piece<float, 4> {
+  typedef float Raw __attribute__((ext_vector_type(4), aligned(4)));
+  static __device__ __forceinline__ void floats(Raw v, float (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = v[i];
+  }
+  static __device__ __forceinline__ Raw raw(const float (&f)[4]) {
+    return Raw{f[0], f[1], f[2], f[3]};
+  }
+};
+template <>
+struct Piece<float, 1> {
+  typedef float Raw;
+  static __device__ __forceinline__ void floats(Raw v, float (&f)[1]) { f[0] = v; }
+  static __device__ __forceinline__ Raw raw(const float (&f)[1]) { return f[0]; }
+};
+
+template <class T, int V>
+__device__ __forceinline__ typename Piece<T, V>::Raw load(const void* base, int64_t at) {
+  return *reinterpret_cast<const typename Piece<T, V>::Raw*>(static_cast<const T*>(base) + at);
+}
+template <class T, int V>
+__device__ __forceinline__ void store(void* base, int64_t at, typename Piece<T, V>::Raw v) {
+  *reinterpret_cast<typename Piece<T, V>::Raw*>(static_cast<T*>(base) + at) = v;
+}
+
+// The row of route r of token t, or -1 (dropped, or past the buffer).
+__device__ __forceinline__ int kept_row(const SortParams& p, int64_t t, int k) {
+  const int row = p.route_row[t * p.top_k + k];
+  return (uint32_t)row < (uint32_t)p.n_rows ? row : -1;
+}
+
+constexpr int kWaves = 4;      // wavefronts per workgroup, each with a run of pieces of its own
+
+// Wavefront u takes pieces [64 P c, 64 P (c + 1)) of token t, u = t * runs + c.
+struct Place {
+  int64_t t;
+  int c;
+};
+template <int P>
+__device__ __forceinline__ bool place(const SortParams& p, int pieces, Place& at) {
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int runs = (pieces + 64 * P - 1) / (64 * P);
+  const int64_t u = (int64_t)blockIdx.x * kWaves + wave;
+  at.t = u / runs;
+  at.c = (int)(u - at.t * runs);
+  return at.t < p.T;
+}
+
+template <class T, int V>
+__global__ __launch_bounds__(64 * kWaves) void sort_kernel(SortParams p) {
+  using R = typename Piece<T, V>::Raw;
+  const int pieces = (p.H + V - 1) / V;
+  Place at;
+  if (!place<1>(p, pieces, at)) return;
+  const int piece = 64 * at.c + ((int)threadIdx.x & 63);
+  if (piece >= pieces) return;
+  const int col = min(piece * V, p.H - V);
+  const R v = load<T, V>(p.x, at.t * p.ld_x + col);
+  for (int k = 0; k < p.top_k; ++k) {
+    const int row = kept_row(p, at.t, k);
+    if (row >= 0) store<T, V>(p.rows, row * p.ld_rows + col, v);
+  }
+}
+
+// Slots in groups of 8: their rows' loads are all on their way before the first is used.
+template <class T, int V, bool WEIGHTED>
+__global__ __launch_bounds__(64 * kWaves) void unsort_kernel(SortParams p) {
+  using R = typename Piece<T, V>::Raw;
+  const int pieces = (p.H + V - 1) / V;
+  Place at;
+  if (!place<1>(p, pieces, at)) return;
+  const int piece = 64 * at.c + ((int)threadIdx.x & 63);
+  if (piece >= pieces) return;
+  const int col = min(piece * V, p.H - V);
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+  for (int k0 = 0; k0 < p.top_k; k0 += 8) {
+    int row[8];
+    float w[8];
+    R v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      row[j] = k0 + j < p.top_k ? kept_row(p, at.t, k0 + j) : -1;
+      w[j] = 1.0f;
+      if (WEIGHTED && k0 + j < p.top_k) w[j] = p.w[at.t * p.top_k + k0 + j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (row[j] >= 0) v[j] = load<T, V>(p.rows, row[j] * p.ld_rows + col);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (row[j] < 0) continue;
+      float f[V];
+      Piece<T, V>::floats(v[j], f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = WEIGHTED ? fmaf(w[j], f[i], acc[i]) : acc[i] + f[i];
+    }
+  }
+  store<T, V>(p.x, at.t * p.ld_x + col, Piece<T, V>::raw(acc));
+}
+
+// Workgroup (t, group of G slots): drows and the dot products of those slots.
+template <class T, int V, int G>
+__global__ __launch_bounds__(64 * kWaves) void unsort_grad_kernel(SortParams p) {
+  using R = typename Piece<T, V>::Raw;
+  __shared__ float sum_s[kWaves][G];
+  const int groups = (p.top_k + G - 1) / G;
+  const int64_t t = blockIdx.x / groups;
+  const int k0 = (int)(blockIdx.x - t * groups) * G;
+  const int tid = threadIdx.x, pieces = (p.H + V - 1) / V;
+  int row[G];
+  float w[G], dot[G];
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    row[j] = k0 + j < p.top_k ? kept_row(p, t, k0 + j) : -1;
+    w[j] = k0 + j < p.top_k ? p.w[t * p.top_k + k0 + j] : 0.0f;
+    dot[j] = 0.0f;
+  }
+  for (int piece = tid; piece < pieces; piece += 64 * kWaves) {
+    const int col = min(piece * V, p.H - V), again = piece * V - col;   // elements counted before
+    const R d = load<T, V>(p.dout, t * p.ld_dout + col);
+    R v[G];
+    if (p.dw) {
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+        if (row[j] >= 0) v[j] = load<T, V>(p.rows, row[j] * p.ld_rows + col);
+    }
+    float g[V];
+    Piece<T, V>::floats(d, g);
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      if (row[j] < 0) continue;
+      if (p.drows) {
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = w[j] * g[i];
+        store<T, V>(p.drows, row[j] * p.ld_drows + col, Piece<T, V>::raw(o));
+      }
+      if (p.dw) {
+        float f[V];
+        Piece<T, V>::floats(v[j], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (V == 1 || i >= again) dot[j] = fmaf(g[i], f[i], dot[j]);
+      }
+    }
+  }
+  if (!p.dw) return;
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    const float s = wave_sum(dot[j]);
+    if ((tid & 63) == 0) sum_s[tid >> 6][j] = s;
+  }
+  __syncthreads();
+  if (tid < G && k0 + tid < p.top_k) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) s += sum_s[i][tid];
+    p.dw[t * p.top_k + k0 + tid] = s;
+  }
+}
+
+bool grid_of(int64_t blocks, dim3& grid) {
+  grid = dim3((unsigned)blocks);
+  return blocks <= 0x7FFFFFFF;
+}
+
+template <class T, int V>
+hipError_t sort_launch(const SortParams& p, SortOp op, hipStream_t stream) {
+  const dim3 block(64 * kWaves);
+  dim3 grid;
+  if (op != SortOp::kGrad) {
+    const int64_t pieces = (p.H + V - 1) / V;
+    if (!grid_of(((int64_t)p.T * ((pieces + 63) / 64) + kWaves - 1) / kWaves, grid))
+      return hipErrorInvalidConfiguration;
+    if (op == SortOp::kSort)
+      hipLaunchKernelGGL((sort_kernel<T, V>), grid, block, 0, stream, p);
+    else if (p.w)
+      hipLaunchKernelGGL((unsort_kernel<T, V, true>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((unsort_kernel<T, V, false>), grid, block, 0, stream, p);
+    return hipGetLastError();
+  }
+  if (!grid_of((int64_t)p.T * ((p.top_k + 3) / 4), grid)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((unsort_grad_kernel<T, V, 4>), grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_sort(const SortParams& p, SortOp op, bool f32, hipStream_t stream) {
+  if (f32)
+    return p.H >= 4 ? sort_launch<float, 4>(p, op, stream) : sort_launch<float, 1>(p, op, stream);
+  return p.H >= 8 ? sort_launch<uint16_t, 8>(p, op, stream)
+                  : sort_launch<uint16_t, 1>(p, op, stream);
+}
+
+}  // namespace mi355moe
