@@ -643,6 +643,10 @@ moe_status_t moe_fp8_linear(const uint16_t* x, int64_t ld_x, const uint8_t* w, c
   if (s != MOE_OK) return s;
   uint8_t* xq = static_cast<uint8_t*>(workspace) + l.xq;
   float* xs = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.xs);
+  if (const int q = fp8_raw_q(M, N, K))
+    return finish(launch_fp8_raw(
+        q, fp8_params(nullptr, K, nullptr, 0, M, w, w_s, M, N, K, out, ld_out, workspace), x, ld_x,
+        stream));
   if (launch_quant_fp8(x, ld_x, M, K, xq, l.ld_q, xs, l.ld_s, stream) != hipSuccess)
     return MOE_ERR_HIP;
   return finish(launch_fp8(

@@ -1,0 +1,137 @@
+// Which kernel, variant and split of K a block-scaled FP8 product takes: host code, from the sizes
+// alone (fp8.hip launches what is picked here).
+#pragma once
+
+#include "dense_pick.h"   // kCus, kMaxSplits, most_partials
+
+namespace mi355moe {
+
+constexpr int kFp8Waves = 16;        // wavefronts of the direct kernels' workgroups
+constexpr int kRawPieces = 4;        // pieces of 8 elements that a thread quantises there
+constexpr int kFp8DirectMost = 512;  // tokens up to which the direct kernel is considered
+constexpr int kFp8DirectRows = 8;    // and up to which it is always taken
+
+// The estimates below, in ns, are fitted to every variant and split of 960 products (M 1 .. 8192,
+// N 64 .. 3584, K 128 .. 7168, log-uniform): what is picked is 2.4% slower than the best of them
+// in the mean, 30% at worst.
+//
+// Direct kernel: a workgroup reads its columns' and tokens' codes at the rate of a CU (with Q = 1
+// half of what it takes with 2: fewer loads are in flight) and takes a fixed time, more where K is
+// longer than its wavefronts take at once; the chip reads weights at about 5600 bytes/ns.  (1 x
+// 3584 x 7168: 7.6 us with Q = 1, 8.4 with 2, 10.4 with 4; 8 x 500 x 2992: 4.3, 3.5, 3.8.)
+struct DirectCost {
+  float rate, fixed, more;
+};
+constexpr DirectCost kFp8Direct[3] = {{67, 1240, 920}, {135, 980, 660}, {47, 900, 300}};
+constexpr DirectCost kFp8Raw[3] = {{72, 1600, 560}, {73, 1370, 600}, {101, 1390, 10}};
+inline float fp8_chip_ns(const DirectCost& c, int q, int M, int N, int K, float bytes, float more) {
+  const int cols = 16 / q;
+  const int64_t wgs = (int64_t)((N + cols - 1) / cols) * ((M + cols - 1) / cols);
+  const float one = bytes / c.rate + c.fixed + (K > 128 * q * kFp8Waves ? c.more : 0.0f) + more;
+  const float cu = (float)((wgs + kCus - 1) / kCus) * one, chip = (float)N * K / 5600.0f;
+  return 1900.0f + (cu > chip ? cu : chip);
+}
+inline float fp8_direct_ns(int i, int M, int N, int K) {
+  const int q = 1 << i, c = 16 / q;
+  return fp8_chip_ns(kFp8Direct[i], q, M, N, K, (float)(c + (M < c ? M : c)) * K, 0.0f);
+}
+inline int fp8_direct_q(int M, int N, int K) {
+  int best = 0;
+  for (int i = 1; i < 3; ++i)
+    if (fp8_direct_ns(i, M, N, K) < fp8_direct_ns(best, M, N, K)) best = i;
+  return 1 << best;
+}
+
+// The tiled kernel's variants: one stage's time with at most one workgroup per CU and with two,
+// and what a workgroup takes besides (first loads, epilogue); a split's join and each partial sum.
+struct Fp8Variant {
+  int bm, bn, per_cu;
+  float one, one_fixed, two, two_fixed, join, part;
+};
+constexpr Fp8Variant kFp8Variants[] = {
+    {256, 256, 1, 1120, 9900, 0, 0, 0, 0},
+    {128, 128, 2, 563, 4400, 965, 6740, 0, 0.0025f},
+    {64, 128, 2, 346, 3265, 644, 4334, 545, 0.0024f},
+    {64, 64, 2, 235, 2160, 446, 2793, 1424, 0.00205f},
+    {32, 64, 2, 206, 1508, 326, 1932, 1880, 0.00184f},
+};
+constexpr int kFp8NumVariants = sizeof(kFp8Variants) / sizeof(kFp8Variants[0]);
+
+inline float fp8_tiled_ns(const Fp8Variant& v, int64_t wgs, int stages) {
+  const int at_once = kCus * v.per_cu, rest = (int)(wgs % at_once);
+  const float one = stages * v.one + v.one_fixed;
+  const float whole = v.per_cu == 2 ? stages * v.two + v.two_fixed : one;
+  return 2000.0f + (float)(wgs / at_once) * whole +
+         (rest == 0 ? 0.0f : rest <= kCus ? one : whole);
+}
+
+struct Fp8Pick {
+  int variant;   // -1: the direct kernel
+  int splits;
+  float ns;      // estimated
+};
+
+inline Fp8Pick fp8_pick(int M, int N, int K) {
+  Fp8Pick best{-1, 1, 3.4e38f};
+  if (M <= kFp8DirectMost) {
+    const int q = fp8_direct_q(M, N, K);
+    best.ns = fp8_direct_ns(q == 1 ? 0 : q == 2 ? 1 : 2, M, N, K);
+  }
+  if (M <= kFp8DirectRows) return best;
+  const int stages = (K + 127) / 128;
+  const int64_t sums = (int64_t)M * ((N + 3) / 4 * 4);
+  // Splits are for launches that leave CUs idle; each has three stages at least.
+  int most = kMaxSplits < stages / 3 ? kMaxSplits : stages / 3;
+  while (most > 1 && most * sums > most_partials(M, N)) --most;
+  for (int i = 0; i < kFp8NumVariants; ++i) {
+    const Fp8Variant& v = kFp8Variants[i];
+    const int64_t tiles = (int64_t)((M + v.bm - 1) / v.bm) * ((N + v.bn - 1) / v.bn);
+    for (int s = 1; s == 1 || (v.per_cu == 2 && s <= most && tiles * s <= 3 * kCus); ++s) {
+      float t = fp8_tiled_ns(v, tiles * s, (stages + s - 1) / s);
+      if (s > 1) t += v.join + v.part * (float)M * N * s;
+      if (t < best.ns) best = {i, s, t};
+    }
+  }
+  return best;
+}
+
+// One launch that quantises every workgroup's tokens anew (its Q), or two (0)?  The estimate of the
+// one, against the other's with 2.7 us for the quantisation, and half a microsecond because a
+// second launch costs the host 3.5 us.  (1 x 3584 x 7168: 8.0 us against 9.9; 64 x 512 x 512 3.9
+// against 6.0; 32 x 3000 x 1024 8.3 against 7.2.)
+inline int fp8_raw(int M, int N, int K) {
+  const int KB = (K + 127) / 128;
+  int best = 0;
+  float least = 0.0f;
+  for (int i = 0; i < 3; ++i) {
+    const int q = 1 << i, c = 16 / q, t = M < c ? M : c;
+    if (t * KB > kRawPieces * 4 * kFp8Waves || M > kFp8DirectMost) continue;
+    const float ns = fp8_chip_ns(kFp8Raw[i], q, M, N, K, (float)(c + 2 * t) * K,
+                                 t * KB > 4 * kFp8Waves ? 1150.0f : 0.0f);
+    if (!best || ns < least) {
+      best = q;
+      least = ns;
+    }
+  }
+  return best && least <= fp8_pick(M, N, K).ns + 3200.0f ? best : 0;
+}
+
+// Grouped: the rows of each expert are known on the GPU only, so as if the R routes were spread
+// evenly over the experts, with half a tile to spare for each.
+inline int fp8_pick_grouped(int R, int E, int N, int K) {
+  const int stages = (K + 127) / 128, used = E < R ? E : R;
+  int best = 0;
+  float least = 3.4e38f;
+  for (int i = 0; i < kFp8NumVariants; ++i) {
+    const Fp8Variant& v = kFp8Variants[i];
+    const int64_t tiles = (int64_t)R / v.bm + (used + 1) / 2;
+    const float t = fp8_tiled_ns(v, (tiles > used ? tiles : used) * ((N + v.bn - 1) / v.bn), stages);
+    if (t < least) {
+      least = t;
+      best = i;
+    }
+  }
+  return best;
+}
+
+}  // namespace mi355moe

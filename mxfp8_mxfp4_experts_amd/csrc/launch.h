@@ -151,6 +151,11 @@ size_t fp8_workspace(int M, int N);   // grows with M
 hipError_t launch_quant_fp8(const uint16_t* x, int64_t ld_x, int T, int H, uint8_t* xq,
                             int64_t ld_q, float* xs, int64_t ld_s, hipStream_t stream);
 hipError_t launch_fp8(const Fp8Params& p, hipStream_t stream);
+// bf16 tokens x in one launch (p.a and p.sa unused), codes made in the product: fp8_raw_q is its Q
+// for these sizes, or 0 where quantisation and product are to be two launches.
+int fp8_raw_q(int M, int N, int K);
+hipError_t launch_fp8_raw(int q, const Fp8Params& p, const uint16_t* x, int64_t ld_x,
+                          hipStream_t stream);
 
 // Tokens into expert order and back (sort.hip).
 enum class SortOp { kSort, kUnsort, kGrad };
