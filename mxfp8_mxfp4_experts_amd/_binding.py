@@ -293,6 +293,22 @@ def moe_route_quant_permute(logits: torch.Tensor, bias: Optional[torch.Tensor], 
 
 def moe_permute(topk_idx: torch.Tensor, expert_offset: int, E_local: int, workspace: torch.Tensor,
                 expert_offsets=None, sorted_route=None, route_row=None):
+    # In front of copies of a few microseconds the checks count: one look at each tensor, and what
+    # is wrong, or only out of the ordinary, is found below.
+    head = _head(topk_idx)
+    if (head is not None and expert_offsets is not None and sorted_route is not None and
+            route_row is not None):
+        idx, T, K = head
+        ptrs = (_plain(topk_idx, torch.int32, T, K, idx),
+                _plain(expert_offsets, torch.int32, E_local + 1, -1, idx),
+                _plain(sorted_route, torch.int32, T * K, -1, idx),
+                _plain(route_row, torch.int32, T * K, -1, idx))
+        if min(ptrs) >= 0:
+            _need(workspace, "workspace", torch.uint8, device=topk_idx.device)
+            _check("moe_permute", (_lib or lib()).moe_permute(
+                ptrs[0], T, K, expert_offset, E_local, *ptrs[1:], workspace.data_ptr(),
+                workspace.numel(), _raw_stream(idx)))
+            return expert_offsets, sorted_route, route_row
     _need(topk_idx, "topk_idx", torch.int32)
     if topk_idx.dim() != 2:
         raise ValueError("topk_idx must be [T, top_k]")

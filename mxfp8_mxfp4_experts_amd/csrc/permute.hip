@@ -20,7 +20,9 @@
 // per 64 experts) turns each expert's chunk counts into the chunks' first rows
 // within the expert and the expert's total, one workgroup scans the totals
 // into expert offsets and tile prefixes, and a rank kernel (one wavefront per
-// chunk) runs the ballot ranking on its chunk from those starting rows.
+// chunk) runs the ballot ranking on its chunk from those starting rows.  Up to
+// 16384 routes all of this is one launch; with few chunks and experts the last
+// three are.
 #include "common.h"
 #include "launch.h"
 #include "permute_dev.h"
@@ -109,10 +111,10 @@ __global__ __launch_bounds__(64 * kColWaves) void perm_colscan_kernel(
 
 // Expert totals -> expert offsets, tile prefixes and the tile -> expert map;
 // grouped rows past the kept count get -1.
-__global__ __launch_bounds__(kPermThreads) void perm_scan_kernel(
-    int R, int E_local, const int32_t* __restrict__ totals,
-    int32_t* __restrict__ expert_offsets, int32_t* __restrict__ sorted_route,
-    int32_t* __restrict__ tile_prefix) {
+__device__ __forceinline__ void perm_scan_block(int R, int E_local, const int32_t* totals,
+                                                int32_t* __restrict__ expert_offsets,
+                                                int32_t* __restrict__ sorted_route,
+                                                int32_t* __restrict__ tile_prefix) {
   __shared__ int wave_tot[kPermWaves][kScanVals];
   __shared__ int n_kept_s;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -178,6 +180,120 @@ __global__ __launch_bounds__(kPermThreads) void perm_scan_kernel(
   for (int r = n_kept + tid; r < R; r += kPermThreads) sorted_route[r] = -1;
 }
 
+__global__ __launch_bounds__(kPermThreads) void perm_scan_kernel(
+    int R, int E_local, const int32_t* __restrict__ totals,
+    int32_t* __restrict__ expert_offsets, int32_t* __restrict__ sorted_route,
+    int32_t* __restrict__ tile_prefix) {
+  perm_scan_block(R, E_local, totals, expert_offsets, sorted_route, tile_prefix);
+}
+
+// One step of the ranking: the rows of 64 routes, lane by lane, from the experts' cursors in LDS.
+__device__ __forceinline__ void rank_step(int r, int r_end, int l, int nbits, int* cursor_s,
+                                          int32_t* __restrict__ sorted_route,
+                                          int32_t* __restrict__ route_row) {
+  const int lane = threadIdx.x & 63;
+  const bool kept = l >= 0;
+  uint64_t peers = __ballot(kept);
+  for (int bit = 0; bit < nbits; ++bit) {
+    const bool set = kept && ((l >> bit) & 1);
+    const uint64_t m = __ballot(set);
+    peers &= set ? m : ~m;
+  }
+  const uint64_t lower = lane ? (~0ull >> (64 - lane)) : 0ull;
+  const int rank = __popcll(peers & lower);
+  const int leader = kept ? (__ffsll((long long)peers) - 1) : lane;
+  int start = 0;
+  if (kept && leader == lane) {
+    start = cursor_s[l];
+    cursor_s[l] = start + __popcll(peers);
+  }
+  start = __shfl(start, leader);
+  if (r < r_end) {
+    if (kept) {
+      const int pos = start + rank;
+      sorted_route[pos] = r;
+      route_row[r] = pos;
+    } else {
+      route_row[r] = -1;
+    }
+  }
+}
+
+// Column scan, scan of the totals and ranking as one launch: every chunk's workgroup adds up the
+// counts of the chunks before its own itself, and one more workgroup writes the schedule.  COUNT:
+// and counts all routes itself, without the count kernel.  (3000 routes over 32 experts: four
+// launches 11.8 us, count and this 6.9, this alone 5.3; 16384 over 28: 7.2 and 7.5; 32768 over 28:
+// 15.8, 9.5 and 12.3; 12000 over 896: 18.2 and 12.3.)
+constexpr int kPermPlaceRoutes = 1 << 14;   // COUNT up to here: as fast, and a launch less
+constexpr int kPermPlaceCounts = 1 << 14;   // without it, the most counts that are added up anew
+constexpr int kPermChunkSteps = 8;   // perm_chunk_size / 64 at most
+template <bool COUNT>
+__global__ __launch_bounds__(kPermThreads) void perm_place_kernel(
+    const int32_t* __restrict__ idx, int R, int offset, int E_local, int chunk, int n_chunks,
+    const int32_t* __restrict__ counts, int32_t* __restrict__ expert_offsets,
+    int32_t* __restrict__ sorted_route, int32_t* __restrict__ route_row,
+    int32_t* __restrict__ tile_prefix) {
+  extern __shared__ int place_s[];
+  int* const total_s = place_s;
+  int* const before_s = place_s + E_local;
+  const int own = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r0 = own * chunk, r_end = min(r0 + chunk, R);
+  int l[kPermChunkSteps];
+  if (wave == 0) {
+#pragma unroll
+    for (int i = 0; i < kPermChunkSteps; ++i)
+      l[i] = local_expert(idx, r0 + 64 * i + lane, r_end, offset, E_local);
+  }
+  for (int e = tid; e < 2 * E_local; e += kPermThreads) place_s[e] = 0;
+  __syncthreads();
+  if constexpr (COUNT) {
+#pragma unroll 4
+    for (int r = tid; r < R; r += kPermThreads) {
+      const int e = local_expert(idx, r, R, offset, E_local);
+      if (e >= 0) {
+        atomicAdd(&total_s[e], 1);
+        if (r < r0) atomicAdd(&before_s[e], 1);
+      }
+    }
+  } else {
+    for (int e = lane; e < E_local; e += 64) {
+      int total = 0, before = 0;
+#pragma unroll 4
+      for (int c = wave; c < n_chunks; c += kPermWaves) {
+        const int v = counts[(size_t)c * E_local + e];
+        total += v;
+        before += c < own ? v : 0;
+      }
+      if (total) atomicAdd(&total_s[e], total);
+      if (before) atomicAdd(&before_s[e], before);
+    }
+  }
+  __syncthreads();
+  if (own == n_chunks) {
+    perm_scan_block(R, E_local, total_s, expert_offsets, sorted_route, tile_prefix);
+    return;
+  }
+  if (wave != 0) return;
+  int run = 0;
+  for (int e0 = 0; e0 < E_local; e0 += 64) {
+    const int e = e0 + lane, own_total = e < E_local ? total_s[e] : 0;
+    int x = own_total;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int y = __shfl_up(x, off);
+      if (lane >= off) x += y;
+    }
+    if (e < E_local) before_s[e] += run + x - own_total;
+    run += __shfl(x, 63);
+  }
+  int nbits = 0;
+  while ((1 << nbits) < E_local) ++nbits;
+#pragma unroll
+  for (int i = 0; i < kPermChunkSteps; ++i)
+    if (r0 + 64 * i < r_end)
+      rank_step(r0 + 64 * i + lane, r_end, l[i], nbits, before_s, sorted_route, route_row);
+}
+
 // Step 3 on one chunk, from the chunk's starting rows (within the expert,
 // plus the expert's offset).
 __global__ __launch_bounds__(64) void perm_rank_kernel(const int32_t* __restrict__ idx, int R,
@@ -197,32 +313,8 @@ __global__ __launch_bounds__(64) void perm_rank_kernel(const int32_t* __restrict
   const int r_end = min(r0 + chunk, R);
   for (int base = r0; base < r_end; base += 64) {
     const int r = base + lane;
-    const int l = local_expert(idx, r, r_end, offset, E_local);
-    const bool kept = l >= 0;
-    uint64_t peers = __ballot(kept);
-    for (int bit = 0; bit < nbits; ++bit) {
-      const bool set = kept && ((l >> bit) & 1);
-      const uint64_t m = __ballot(set);
-      peers &= set ? m : ~m;
-    }
-    const uint64_t lower = lane ? (~0ull >> (64 - lane)) : 0ull;
-    const int rank = __popcll(peers & lower);
-    const int leader = kept ? (__ffsll((long long)peers) - 1) : lane;
-    int start = 0;
-    if (kept && leader == lane) {
-      start = cursor_s[l];
-      cursor_s[l] = start + __popcll(peers);
-    }
-    start = __shfl(start, leader);
-    if (r < r_end) {
-      if (kept) {
-        const int pos = start + rank;
-        sorted_route[pos] = r;
-        route_row[r] = pos;
-      } else {
-        route_row[r] = -1;
-      }
-    }
+    rank_step(r, r_end, local_expert(idx, r, r_end, offset, E_local), nbits, cursor_s, sorted_route,
+              route_row);
   }
 }
 
@@ -240,8 +332,21 @@ hipError_t launch_permute(const int32_t* idx, int R, int offset, int E_local, in
   }
   const int n_chunks = perm_chunks(R), chunk = perm_chunk_size(R);
   const size_t lds = sizeof(int) * (size_t)E_local;
+  const dim3 place_grid(n_chunks + 1), place_block(kPermThreads);
+  if (R <= kPermPlaceRoutes) {
+    hipLaunchKernelGGL((perm_place_kernel<true>), place_grid, place_block, 2 * lds, stream, idx, R,
+                       offset, E_local, chunk, n_chunks, counts, offs, sorted_route, route_row,
+                       tile_prefix);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(perm_count_kernel, dim3(n_chunks), dim3(256), lds, stream, idx, R, offset,
                      E_local, chunk, counts);
+  if ((int64_t)n_chunks * E_local <= kPermPlaceCounts) {
+    hipLaunchKernelGGL((perm_place_kernel<false>), place_grid, place_block, 2 * lds, stream, idx, R,
+                       offset, E_local, chunk, n_chunks, counts, offs, sorted_route, route_row,
+                       tile_prefix);
+    return hipGetLastError();
+  }
   int32_t* const totals = counts + (size_t)n_chunks * E_local;
   hipLaunchKernelGGL(perm_colscan_kernel, dim3((E_local + 63) / 64), dim3(64 * kColWaves), 0, stream,
                      E_local, n_chunks, counts, totals);
