@@ -8,7 +8,14 @@
 //
 // All three run token by token, so that what a token's routes share (x[t], out[t], dout[t]) is
 // read or written once and what they differ in moves as whole rows; nothing is added with
-// atomics, and equal calls give equal bits.  Memory bounds them at many tokens.
+// atomics, and equal calls give equal bits.
+//
+// Memory bounds them at many tokens: 4096 tokens x 8 routes x 3584 in bf16, sort 264 MB in 45 us, 5.9
+// TB/s; unsort 50 us, 5.3; gradients 499 MB in 90 us, 5.5 (a copy of 2 GiB reaches 5.0).  That takes
+// loads and stores that leave the caches alone (NT): with plain ones 51, 56 and 99 us.  Rows that
+// the caches hold for what comes next, or from what came before, are left in them: 256 tokens x 8
+// (15 MB) unsort 5.9 us plain and 7.2 past the caches.  At few tokens the chain of place, load and
+// store bounds them: 8 x 16 x 7168 sort 3.6 us, unsort 5.0.
 //
 // A row is cut into pieces of 16 bytes.  Rows may start at any element and have any length: the
 // pieces are accessed at element alignment (gfx950 takes that), and a row's last piece is moved
@@ -66,13 +73,20 @@ struct Piece<float, 1> {
   static __device__ __forceinline__ Raw raw(const float (&f)[1]) { return f[0]; }
 };
 
-template <class T, int V>
+template <class T, int V, bool NT = false>
 __device__ __forceinline__ typename Piece<T, V>::Raw load(const void* base, int64_t at) {
-  return *reinterpret_cast<const typename Piece<T, V>::Raw*>(static_cast<const T*>(base) + at);
+  const auto* q =
+      reinterpret_cast<const typename Piece<T, V>::Raw*>(static_cast<const T*>(base) + at);
+  if constexpr (NT) return __builtin_nontemporal_load(q);
+  return *q;
 }
-template <class T, int V>
+template <class T, int V, bool NT = false>
 __device__ __forceinline__ void store(void* base, int64_t at, typename Piece<T, V>::Raw v) {
-  *reinterpret_cast<typename Piece<T, V>::Raw*>(static_cast<T*>(base) + at) = v;
+  auto* q = reinterpret_cast<typename Piece<T, V>::Raw*>(static_cast<T*>(base) + at);
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, q);
+  else
+    *q = v;
 }
 
 // The row of route r of token t, or -1 (dropped, or past the buffer).
@@ -83,65 +97,71 @@ __device__ __forceinline__ int kept_row(const SortParams& p, int64_t t, int k) {
 
 constexpr int kWaves = 4;      // wavefronts per workgroup, each with a run of pieces of its own
 
-// Wavefront u takes pieces [64 P c, 64 P (c + 1)) of token t, u = t * runs + c.
+// Wavefront u takes pieces [64 c, 64 (c + 1)) of token t, u = t * runs + c.
 struct Place {
   int64_t t;
   int c;
 };
-template <int P>
 __device__ __forceinline__ bool place(const SortParams& p, int pieces, Place& at) {
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int runs = (pieces + 64 * P - 1) / (64 * P);
+  const int runs = (pieces + 63) / 64;
   const int64_t u = (int64_t)blockIdx.x * kWaves + wave;
   at.t = u / runs;
   at.c = (int)(u - at.t * runs);
   return at.t < p.T;
 }
 
-template <class T, int V>
+// The places of G slots from k0 on are known before the first is used.
+template <class T, int V, bool NT>
 __global__ __launch_bounds__(64 * kWaves) void sort_kernel(SortParams p) {
   using R = typename Piece<T, V>::Raw;
+  constexpr int G = 8;
   const int pieces = (p.H + V - 1) / V;
   Place at;
-  if (!place<1>(p, pieces, at)) return;
+  if (!place(p, pieces, at)) return;
   const int piece = 64 * at.c + ((int)threadIdx.x & 63);
   if (piece >= pieces) return;
   const int col = min(piece * V, p.H - V);
   const R v = load<T, V>(p.x, at.t * p.ld_x + col);
-  for (int k = 0; k < p.top_k; ++k) {
-    const int row = kept_row(p, at.t, k);
-    if (row >= 0) store<T, V>(p.rows, row * p.ld_rows + col, v);
+  for (int k0 = 0; k0 < p.top_k; k0 += G) {
+    int row[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) row[j] = k0 + j < p.top_k ? kept_row(p, at.t, k0 + j) : -1;
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+      if (row[j] >= 0) store<T, V, NT>(p.rows, row[j] * p.ld_rows + col, v);
   }
 }
 
-// Slots in groups of 8: their rows' loads are all on their way before the first is used.
-template <class T, int V, bool WEIGHTED>
+// Slots in groups of G: their rows' loads are all on their way before the first is used.
+template <class T, int V, bool WEIGHTED, bool NT>
 __global__ __launch_bounds__(64 * kWaves) void unsort_kernel(SortParams p) {
   using R = typename Piece<T, V>::Raw;
+  constexpr int G = 8;
   const int pieces = (p.H + V - 1) / V;
   Place at;
-  if (!place<1>(p, pieces, at)) return;
+  if (!place(p, pieces, at)) return;
   const int piece = 64 * at.c + ((int)threadIdx.x & 63);
   if (piece >= pieces) return;
   const int col = min(piece * V, p.H - V);
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-  for (int k0 = 0; k0 < p.top_k; k0 += 8) {
-    int row[8];
-    float w[8];
-    R v[8];
+  for (int k0 = 0; k0 < p.top_k; k0 += G) {
+    int row[G];
+    float w[G];
+    R v[G];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < G; ++j) {
       row[j] = k0 + j < p.top_k ? kept_row(p, at.t, k0 + j) : -1;
       w[j] = 1.0f;
       if (WEIGHTED && k0 + j < p.top_k) w[j] = p.w[at.t * p.top_k + k0 + j];
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (row[j] >= 0) v[j] = load<T, V>(p.rows, row[j] * p.ld_rows + col);
+    for (int j = 0; j < G; ++j)
+      if (row[j] >= 0) v[j] = load<T, V, NT>(p.rows, row[j] * p.ld_rows + col);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < G; ++j) {
       if (row[j] < 0) continue;
       float f[V];
       Piece<T, V>::floats(v[j], f);
@@ -152,15 +172,19 @@ __global__ __launch_bounds__(64 * kWaves) void unsort_kernel(SortParams p) {
   store<T, V>(p.x, at.t * p.ld_x + col, Piece<T, V>::raw(acc));
 }
 
-// Workgroup (t, group of G slots): drows and the dot products of those slots.
-template <class T, int V, int G>
+// Unit (token, group of G slots): drows and the dot products of those slots, by a workgroup (WAVE
+// false) or, for rows of few pieces, by a wavefront.
+template <class T, int V, int G, bool WAVE, bool NT>
 __global__ __launch_bounds__(64 * kWaves) void unsort_grad_kernel(SortParams p) {
   using R = typename Piece<T, V>::Raw;
   __shared__ float sum_s[kWaves][G];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int groups = (p.top_k + G - 1) / G;
-  const int64_t t = blockIdx.x / groups;
-  const int k0 = (int)(blockIdx.x - t * groups) * G;
-  const int tid = threadIdx.x, pieces = (p.H + V - 1) / V;
+  const int64_t unit = WAVE ? (int64_t)blockIdx.x * kWaves + wave : (int64_t)blockIdx.x;
+  const int64_t t = unit / groups;
+  if (t >= p.T) return;
+  const int k0 = (int)(unit - t * groups) * G;
+  const int pieces = (p.H + V - 1) / V;
   int row[G];
   float w[G], dot[G];
 #pragma unroll
@@ -169,14 +193,14 @@ __global__ __launch_bounds__(64 * kWaves) void unsort_grad_kernel(SortParams p) 
     w[j] = k0 + j < p.top_k ? p.w[t * p.top_k + k0 + j] : 0.0f;
     dot[j] = 0.0f;
   }
-  for (int piece = tid; piece < pieces; piece += 64 * kWaves) {
+  for (int piece = WAVE ? lane : tid; piece < pieces; piece += WAVE ? 64 : 64 * kWaves) {
     const int col = min(piece * V, p.H - V), again = piece * V - col;   // elements counted before
     const R d = load<T, V>(p.dout, t * p.ld_dout + col);
     R v[G];
     if (p.dw) {
 #pragma unroll
       for (int j = 0; j < G; ++j)
-        if (row[j] >= 0) v[j] = load<T, V>(p.rows, row[j] * p.ld_rows + col);
+        if (row[j] >= 0) v[j] = load<T, V, NT>(p.rows, row[j] * p.ld_rows + col);
     }
     float g[V];
     Piece<T, V>::floats(d, g);
@@ -187,7 +211,7 @@ __global__ __launch_bounds__(64 * kWaves) void unsort_grad_kernel(SortParams p) 
         float o[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) o[i] = w[j] * g[i];
-        store<T, V>(p.drows, row[j] * p.ld_drows + col, Piece<T, V>::raw(o));
+        store<T, V, NT>(p.drows, row[j] * p.ld_drows + col, Piece<T, V>::raw(o));
       }
       if (p.dw) {
         float f[V];
@@ -199,18 +223,22 @@ __global__ __launch_bounds__(64 * kWaves) void unsort_grad_kernel(SortParams p) 
     }
   }
   if (!p.dw) return;
+  float mine = 0.0f;                        // lane j: slot j's
 #pragma unroll
   for (int j = 0; j < G; ++j) {
     const float s = wave_sum(dot[j]);
-    if ((tid & 63) == 0) sum_s[tid >> 6][j] = s;
+    if (lane == j) mine = s;
   }
-  __syncthreads();
-  if (tid < G && k0 + tid < p.top_k) {
-    float s = 0.0f;
+  if constexpr (!WAVE) {
+    if (lane < G) sum_s[wave][lane] = mine;
+    __syncthreads();
+    if (tid < G) {
+      mine = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) s += sum_s[i][tid];
-    p.dw[t * p.top_k + k0 + tid] = s;
+      for (int i = 0; i < kWaves; ++i) mine += sum_s[i][tid];
+    }
   }
+  if ((WAVE ? lane : tid) < G && k0 + lane < p.top_k) p.dw[t * p.top_k + k0 + lane] = mine;
 }
 
 bool grid_of(int64_t blocks, dim3& grid) {
@@ -218,25 +246,46 @@ bool grid_of(int64_t blocks, dim3& grid) {
   return blocks <= 0x7FFFFFFF;
 }
 
-template <class T, int V>
+// Rows of more bytes than this go past the caches.  (Gradients of 1024 tokens x 8 x 3584 in bf16, 59
+// MB: 25.9 us with plain loads and stores, 24.4 past the caches; unsort 12.7 and 12.7; of 2048, 117
+// MB: 51.7 and 47.0; 30.2 and 25.6.)
+constexpr int64_t kCached = 64 << 20;
+// Slots of a token that one unit of the gradients takes: with 8 instead of 4, 8 tokens x 16 slots
+// take 8.5 us instead of 5.9 and 4096 x 8 93 instead of 90.
+constexpr int kGradSlots = 4;
+
+template <class T, int V, bool NT>
 hipError_t sort_launch(const SortParams& p, SortOp op, hipStream_t stream) {
   const dim3 block(64 * kWaves);
   dim3 grid;
+  const int64_t pieces = (p.H + V - 1) / V;
   if (op != SortOp::kGrad) {
-    const int64_t pieces = (p.H + V - 1) / V;
     if (!grid_of(((int64_t)p.T * ((pieces + 63) / 64) + kWaves - 1) / kWaves, grid))
       return hipErrorInvalidConfiguration;
     if (op == SortOp::kSort)
-      hipLaunchKernelGGL((sort_kernel<T, V>), grid, block, 0, stream, p);
+      hipLaunchKernelGGL((sort_kernel<T, V, NT>), grid, block, 0, stream, p);
     else if (p.w)
-      hipLaunchKernelGGL((unsort_kernel<T, V, true>), grid, block, 0, stream, p);
+      hipLaunchKernelGGL((unsort_kernel<T, V, true, NT>), grid, block, 0, stream, p);
     else
-      hipLaunchKernelGGL((unsort_kernel<T, V, false>), grid, block, 0, stream, p);
+      hipLaunchKernelGGL((unsort_kernel<T, V, false, NT>), grid, block, 0, stream, p);
     return hipGetLastError();
   }
-  if (!grid_of((int64_t)p.T * ((p.top_k + 3) / 4), grid)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((unsort_grad_kernel<T, V, 4>), grid, block, 0, stream, p);
+  constexpr int G = kGradSlots;
+  const int64_t units = (int64_t)p.T * ((p.top_k + G - 1) / G);
+  const bool wave = pieces <= 64;   // 8192 x 2 x 512 in bf16: 9.9 us by workgroups, 5.4 so
+  if (!grid_of(wave ? (units + kWaves - 1) / kWaves : units, grid))
+    return hipErrorInvalidConfiguration;
+  if (wave)
+    hipLaunchKernelGGL((unsort_grad_kernel<T, V, G, true, NT>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((unsort_grad_kernel<T, V, G, false, NT>), grid, block, 0, stream, p);
   return hipGetLastError();
+}
+template <class T, int V>
+hipError_t sort_launch(const SortParams& p, SortOp op, hipStream_t stream) {
+  const int64_t rows = (int64_t)p.T * p.top_k < p.n_rows ? (int64_t)p.T * p.top_k : p.n_rows;
+  return rows * p.H * (int64_t)sizeof(T) > kCached ? sort_launch<T, V, true>(p, op, stream)
+                                                   : sort_launch<T, V, false>(p, op, stream);
 }
 
 }  // namespace

@@ -121,6 +121,7 @@ CASES = [
     (40, 3, 6, 3, 512, "masked"), (64, 2, 3, 3, 513, ""), (100, 17, 30, 10, 1037, ""),
     (20, 64, 64, 40, 130, ""), (50, 4, 4, 4, 2050, "repeats"), (12, 3, 8, 8, 40, "none"),
     (1000, 8, 28, 28, 520, ""), (3000, 2, 64, 8, 72, ""),
+    (4200, 8, 28, 28, 1301, ""), (5000, 7, 20, 10, 1025, "masked"),   # past the caches
 ]
 
 
