@@ -494,8 +494,7 @@ moe_status_t moe_route_groups(const float* logits, int64_t ld_logits, const floa
  *        is xs[b, m] (tokens side by side: the products read one block of many
  *        tokens at a time).
  *   w    E4M3 [N, K]; w_s float [NB, KB]; experts one after another.
- *   out  bf16 [M, N], row stride ld_out (>= N), 16-byte aligned; vector stores
- *        where ld_out is a multiple of 4.
+ *   out  bf16 [M, N], row stride ld_out (>= N, any), 16-byte aligned.
  *   out[m, n] = sum_b (xs[b, m] * w_s[n / 128, b]) * (sum_{k in b} xq[m, k] w[n, k])
  *   rounded once to bf16; the scales' product and the sum over blocks in float,
  *   the sum within a block by the matrix unit, whose accumulation keeps about

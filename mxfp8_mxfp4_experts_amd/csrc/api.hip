@@ -94,7 +94,7 @@ Fp8Layout fp8_layout(int M, int N, int K) {
 Fp8Params fp8_params(const uint8_t* xq, int64_t ld_xq, const float* xs, int64_t ld_xs, int rows,
                      const uint8_t* w, const float* w_s, int M, int N, int K, uint16_t* out,
                      int64_t ld_out, void* workspace) {
-  return Fp8Params{xq, ld_xq, xs, ld_xs, w, w_s, M, N, K, out, ld_out, ld_out % 4 == 0, workspace,
+  return Fp8Params{xq, ld_xq, xs, ld_xs, w, w_s, M, N, K, out, ld_out, workspace,
                    1, nullptr, nullptr, 1, rows};
 }
 

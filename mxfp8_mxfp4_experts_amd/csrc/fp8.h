@@ -19,16 +19,17 @@ __device__ __forceinline__ v4f mfma_fp8(v4i b_lo, v4i b_hi, v4i a_lo, v4i a_hi) 
                                                           0, 0, 0, 0);
 }
 
-// Columns n .. n + 3 of output row m, as one store where the row's place allows it.
+// Columns n .. n + 3 of output row m, as one store at element alignment unless the row ends.
 __device__ __forceinline__ void fp8_store(const Fp8Params& p, v4f s, int64_t m, int n) {
+  typedef uint32_t any2 __attribute__((ext_vector_type(2), aligned(2)));
   if (n >= p.N) return;
   uint16_t* o = p.out + m * p.ld_out + n;
-  const uint2 h = make_uint2(f32x2_to_bf16x2(s[0], s[1]), f32x2_to_bf16x2(s[2], s[3]));
-  if (p.out_vec && n + 4 <= p.N) {
-    *reinterpret_cast<uint2*>(o) = h;
+  const any2 h = {f32x2_to_bf16x2(s[0], s[1]), f32x2_to_bf16x2(s[2], s[3])};
+  if (n + 4 <= p.N) {
+    *reinterpret_cast<any2*>(o) = h;
   } else {
-    const uint64_t h4 = ((uint64_t)h.y << 32) | h.x;
-    for (int j = 0; j < 4 && n + j < p.N; ++j) o[j] = (uint16_t)(h4 >> (16 * j));
+    const uint64_t h4 = ((uint64_t)h[1] << 32) | h[0];
+    for (int j = 0; j < 3 && n + j < p.N; ++j) o[j] = (uint16_t)(h4 >> (16 * j));
   }
 }
 

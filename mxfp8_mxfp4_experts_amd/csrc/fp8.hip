@@ -32,26 +32,41 @@ __device__ __forceinline__ uint2 fp8x8(const float (&f)[8], float inv, bool odd)
                     e4m3x4_scaled(q[4], q[5], q[6], q[7], 1.0f));
 }
 
-// Eight elements per lane; 16 lanes share a block of 128.
+// Eight elements per lane; 16 lanes share a block of 128.  A wavefront takes kUnits units of 512
+// elements of a row, units in a row's order, its loads all at once.
+constexpr int kQuantUnits = 2;
 __global__ __launch_bounds__(256) void quant_fp8_kernel(const uint16_t* __restrict__ x,
-                                                        int64_t ld_x, int T, int H,
+                                                        int64_t ld_x, int T, int H, int per_row,
                                                         uint8_t* __restrict__ xq, int64_t ld_q,
                                                         float* __restrict__ xs, int64_t ld_s) {
-  const int KB = (H + kScaleBlock - 1) / kScaleBlock;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t t = at / (16 * KB);
-  if (t >= T) return;                     // alike for a block's 16 lanes
-  const int c = (int)(at - t * (16 * KB)), k = 8 * c;
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (k < H) v = *reinterpret_cast<const uint4*>(x + t * ld_x + k);
-  uint32_t top = absmax8_bits(v);         // a NaN counts as the largest
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const uint32_t first = (blockIdx.x * 4u + wave) * kQuantUnits;
+  uint4 v[kQuantUnits];
+  int64_t t[kQuantUnits];
+  int k[kQuantUnits];
 #pragma unroll
-  for (int i = 1; i < 16; i <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, i));
-  float inv, f[8];
-  const float s = fp8_scale(__uint_as_float(top), inv);
-  unpack8(v, f);
-  if (k < H) *reinterpret_cast<uint2*>(xq + t * ld_q + k) = fp8x8(f, inv, !(s == s));
-  if ((c & 15) == 0) xs[(c >> 4) * ld_s + t] = s;
+  for (int i = 0; i < kQuantUnits; ++i) {
+    const uint32_t u = first + i;
+    t[i] = u / (uint32_t)per_row;
+    k[i] = 512 * (int)(u - (uint32_t)t[i] * (uint32_t)per_row) + 8 * lane;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (t[i] < T && k[i] < H) v[i] = *reinterpret_cast<const uint4*>(x + t[i] * ld_x + k[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kQuantUnits; ++i) {
+    if (t[i] >= T) return;                  // alike for the wavefront
+    uint32_t top = absmax8_bits(v[i]);      // a NaN counts as the largest
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    float inv, f[8];
+    const float s = fp8_scale(__uint_as_float(top), inv);
+    unpack8(v[i], f);
+    if (k[i] < H) {
+      *reinterpret_cast<uint2*>(xq + t[i] * ld_q + k[i]) = fp8x8(f, inv, !(s == s));
+      if (lane % 16 == 0) xs[(k[i] / kScaleBlock) * ld_s + t[i]] = s;
+    }
+  }
 }
 
 // 16 bytes at k of a row of K bytes, zeros past its end (the load itself is unconditional).
@@ -311,11 +326,11 @@ __global__ __launch_bounds__(64) void fp8_far_kernel(Fp8Params p) {
 
 hipError_t launch_quant_fp8(const uint16_t* x, int64_t ld_x, int T, int H, uint8_t* xq,
                             int64_t ld_q, float* xs, int64_t ld_s, hipStream_t stream) {
-  const int64_t lanes = (int64_t)T * 16 * ((H + kScaleBlock - 1) / kScaleBlock);
-  const int64_t blocks = (lanes + 255) / 256;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const int per_row = (H + 511) / 512;
+  const int64_t units = (int64_t)T * per_row, blocks = (units + 4 * kQuantUnits - 1) / (4 * kQuantUnits);
+  if (units > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(quant_fp8_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x, ld_x, T, H,
-                     xq, ld_q, xs, ld_s);
+                     per_row, xq, ld_q, xs, ld_s);
   return hipGetLastError();
 }
 

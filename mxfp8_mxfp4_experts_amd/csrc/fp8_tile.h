@@ -439,73 +439,56 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
       }
     return;
   }
-  if (p.out_vec && t.n0 + BN <= p.N) {
+  // Rows start at any element (8- and 16-byte stores at element alignment).
+  typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
+  typedef uint32_t any2 __attribute__((ext_vector_type(2), aligned(2)));
+  if (t.n0 + BN <= p.N) {
     // Whole columns: 8 bytes per lane, or 16 after a swap between lane rows (two column blocks
     // at a time: each lane then has 8 neighbouring columns, 64 bytes of a row per store).
     auto pack = [&](int i, int j) __attribute__((always_inline)) {
       return make_uint2(f32x2_to_bf16x2(acc[i][j][0], acc[i][j][1]),
                         f32x2_to_bf16x2(acc[i][j][2], acc[i][j][3]));
     };
-    int j0 = 0;
-    if constexpr (NI > 1) {
-      if ((p.ld_out & 7) == 0) {
-        uint16_t* o2 = p.out + m_w * p.ld_out + n_wave + 16 * (g & 1) + 8 * (g >> 1);
+    uint16_t* o2 = p.out + m_w * p.ld_out + n_wave + 16 * (g & 1) + 8 * (g >> 1);
 #pragma unroll
-        for (int j = 0; j + 1 < NI; j += 2)
+    for (int j = 0; j + 1 < NI; j += 2)
 #pragma unroll
-          for (int i = 0; i < MI; ++i) {
-            const uint2 u = pack(i, j), v = pack(i, j + 1);
-            const auto x = __builtin_amdgcn_permlane16_swap(u.x, v.x, false, false);
-            const auto y = __builtin_amdgcn_permlane16_swap(u.y, v.y, false, false);
-            if (m_w + 16 * i < t.m1)
-              *reinterpret_cast<uint4*>(o2 + 16 * i * p.ld_out + 16 * j) =
-                  make_uint4(x[0], y[0], x[1], y[1]);
-          }
-        j0 = NI & ~1;
-      }
-    }
-    uint16_t* o = p.out + m_w * p.ld_out + n_w;
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      if (j < j0) continue;
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int i = 0; i < MI; ++i) {
+        const uint2 u = pack(i, j), v = pack(i, j + 1);
+        const auto x = __builtin_amdgcn_permlane16_swap(u.x, v.x, false, false);
+        const auto y = __builtin_amdgcn_permlane16_swap(u.y, v.y, false, false);
         if (m_w + 16 * i < t.m1)
-          *reinterpret_cast<uint2*>(o + 16 * i * p.ld_out + 16 * j) = pack(i, j);
+          *reinterpret_cast<any4*>(o2 + 16 * i * p.ld_out + 16 * j) = any4{x[0], y[0], x[1], y[1]};
+      }
+    if constexpr (NI % 2 == 1) {
+      uint16_t* o = p.out + m_w * p.ld_out + n_w + 16 * (NI - 1);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const uint2 u = pack(i, NI - 1);
+        if (m_w + 16 * i < t.m1) *reinterpret_cast<any2*>(o + 16 * i * p.ld_out) = any2{u.x, u.y};
+      }
     }
     return;
   }
-  // A tile at the columns' edge, or rows that take no vector stores: through LDS (each wavefront
-  // its own part, 16 rows at a time), so that a store instruction writes neighbouring elements.
-  asm volatile("s_barrier" ::: "memory");   // the ring is no longer read
-  constexpr int kRow = 16 * NI + 4;         // floats; the pad spreads the rows over the banks
-  static_assert(G::W * 16 * kRow * 4 <= G::kLds, "epilogue rows fit in the ring");
-  float* rows = reinterpret_cast<float*>(lds) + wave * 16 * kRow;
-  constexpr int kRows = NI < 4 ? 4 / NI : 1, kColSteps = (16 * NI + 63) / 64;
-  const int row0 = NI < 4 ? lane / (16 * NI) : 0, col0 = NI < 4 ? lane % (16 * NI) : lane;
+  // A tile at the columns' edge: four columns at a time, the last ones one by one.
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
+    if (m_w + 16 * i >= t.m1) continue;
+    uint16_t* o = p.out + (m_w + 16 * i) * p.ld_out + n_w;
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
-      *reinterpret_cast<v4f*>(rows + r * kRow + 16 * j + 4 * g) = acc[i][j];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll 4
-    for (int row = row0; row < 16; row += kRows) {
-      const int64_t m = t.m0 + 16 * MI * wm + 16 * i + row;
-      if (m >= t.m1) continue;
-      uint16_t* o = p.out + m * p.ld_out + n_wave;
+    for (int j = 0; j < NI; ++j) {
+      const uint32_t lo = f32x2_to_bf16x2(acc[i][j][0], acc[i][j][1]);
+      const uint32_t hi = f32x2_to_bf16x2(acc[i][j][2], acc[i][j][3]);
+      const int n = n_w + 16 * j;
+      if (n + 4 <= p.N) {
+        *reinterpret_cast<any2*>(o + 16 * j) = any2{lo, hi};
+      } else {
+        const uint64_t h = ((uint64_t)hi << 32) | lo;
 #pragma unroll
-      for (int c = 0; c < kColSteps; ++c) {
-        const int col = col0 + 64 * c;
-        if (col < 16 * NI && n_wave + col < p.N)
-          o[col] = (uint16_t)f32x2_to_bf16x2(rows[row * kRow + col], 0.0f);
+        for (int e = 0; e < 3; ++e)
+          if (n + e < p.N) o[16 * j + e] = (uint16_t)(h >> (16 * e));
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
 }
 

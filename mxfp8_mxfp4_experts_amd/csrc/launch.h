@@ -138,7 +138,6 @@ struct Fp8Params {
   int M, N, K;              // M: rows of out
   uint16_t* out;
   int64_t ld_out;
-  int out_vec;              // rows take 4-element vector stores
   void* partial;            // dense: fp8_workspace bytes
   // Grouped (offs null: dense).
   int E;
