@@ -11,9 +11,9 @@ constexpr int kRawPieces = 4;        // pieces of 8 elements that a thread quant
 constexpr int kFp8DirectMost = 512;  // tokens up to which the direct kernel is considered
 constexpr int kFp8DirectRows = 8;    // and up to which it is always taken
 
-// The estimates below, in ns, are fitted to every variant and split of 960 products (M 1 .. 8192,
-// N 64 .. 3584, K 128 .. 7168, log-uniform): what is picked is 2.4% slower than the best of them
-// in the mean, 30% at worst.
+// The estimates below, in ns, are fitted to every variant and split of 900 products (M 1 .. 8192,
+// N 64 .. 3584, K 128 .. 7168, log-uniform): what is picked is 2.2% slower than the best of them
+// in the mean, 43% at worst.
 //
 // Direct kernel: a workgroup reads its columns' and tokens' codes at the rate of a CU (with Q = 1
 // half of what it takes with 2: fewer loads are in flight) and takes a fixed time, more where K is
@@ -22,8 +22,8 @@ constexpr int kFp8DirectRows = 8;    // and up to which it is always taken
 struct DirectCost {
   float rate, fixed, more;
 };
-constexpr DirectCost kFp8Direct[3] = {{67, 1240, 920}, {135, 980, 660}, {47, 900, 300}};
-constexpr DirectCost kFp8Raw[3] = {{72, 1600, 560}, {73, 1370, 600}, {101, 1390, 10}};
+constexpr DirectCost kFp8Direct[3] = {{61, 1160, 720}, {130, 1020, 680}, {46, 910, 300}};
+constexpr DirectCost kFp8Raw[3] = {{72, 1540, 520}, {106, 1410, 650}, {77, 1390, 300}};
 inline float fp8_chip_ns(const DirectCost& c, int q, int M, int N, int K, float bytes, float more) {
   const int cols = 16 / q;
   const int64_t wgs = (int64_t)((N + cols - 1) / cols) * ((M + cols - 1) / cols);
@@ -42,27 +42,27 @@ inline int fp8_direct_q(int M, int N, int K) {
   return 1 << best;
 }
 
-// The tiled kernel's variants: one stage's time with at most one workgroup per CU and with two,
-// and what a workgroup takes besides (first loads, epilogue); a split's join and each partial sum.
+// The tiled kernel's variants: one stage's time in launches of up to half the workgroups that run
+// at once and in fuller ones (one and two per CU; of 256 x 256 tiles half a workgroup and one), and
+// what a workgroup takes besides (first loads, epilogue); a split's join and each partial sum.
 struct Fp8Variant {
   int bm, bn, per_cu;
   float one, one_fixed, two, two_fixed, join, part;
 };
 constexpr Fp8Variant kFp8Variants[] = {
-    {256, 256, 1, 1120, 9900, 0, 0, 0, 0},
-    {128, 128, 2, 563, 4400, 965, 6740, 0, 0.0025f},
-    {64, 128, 2, 346, 3265, 644, 4334, 545, 0.0024f},
-    {64, 64, 2, 235, 2160, 446, 2793, 1424, 0.00205f},
-    {32, 64, 2, 206, 1508, 326, 1932, 1880, 0.00184f},
+    {256, 256, 1, 1136, 5840, 1451, 10090, 0, 0},
+    {128, 128, 2, 547, 2627, 1060, 4957, 1129, 0.0029f},
+    {64, 128, 2, 338, 1936, 704, 3020, 1744, 0.0023f},
+    {64, 64, 2, 232, 1467, 463, 2103, 1993, 0.0021f},
+    {32, 64, 2, 194, 1100, 321, 1614, 2128, 0.0019f},
 };
 constexpr int kFp8NumVariants = sizeof(kFp8Variants) / sizeof(kFp8Variants[0]);
 
 inline float fp8_tiled_ns(const Fp8Variant& v, int64_t wgs, int stages) {
   const int at_once = kCus * v.per_cu, rest = (int)(wgs % at_once);
-  const float one = stages * v.one + v.one_fixed;
-  const float whole = v.per_cu == 2 ? stages * v.two + v.two_fixed : one;
-  return 2000.0f + (float)(wgs / at_once) * whole +
-         (rest == 0 ? 0.0f : rest <= kCus ? one : whole);
+  const float one = stages * v.one + v.one_fixed, two = stages * v.two + v.two_fixed;
+  return 2000.0f + (float)(wgs / at_once) * two +
+         (rest == 0 ? 0.0f : rest <= at_once / 2 && rest <= kCus ? one : two);
 }
 
 struct Fp8Pick {
@@ -107,7 +107,7 @@ inline int fp8_raw(int M, int N, int K) {
     const int q = 1 << i, c = 16 / q, t = M < c ? M : c;
     if (t * KB > kRawPieces * 4 * kFp8Waves || M > kFp8DirectMost) continue;
     const float ns = fp8_chip_ns(kFp8Raw[i], q, M, N, K, (float)(c + 2 * t) * K,
-                                 t * KB > 4 * kFp8Waves ? 1150.0f : 0.0f);
+                                 t * KB > 4 * kFp8Waves ? 1280.0f : 0.0f);
     if (!best || ns < least) {
       best = q;
       least = ns;
