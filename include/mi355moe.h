@@ -587,7 +587,8 @@ moe_status_t moe_unsort_tokens(const void* rows, int64_t ld_rows, int n_rows, in
  *   dw[t, k] = sum_h dout[t, h] * rows[route_row[t, k], h] in float (0 for a
  *   route that is not kept).
  *   drows [n_rows, H], row stride ld_drows, or NULL for none; dw float [T,
- *   top_k], or NULL for none (rows is not read then); at least one of the two. */
+ *   top_k], or NULL for none (rows is not read then); at least one of the two;
+ *   no overlap. */
 moe_status_t moe_unsort_tokens_grad(const void* dout, int64_t ld_dout, const void* rows,
                                     int64_t ld_rows, int n_rows, int T, int H, int top_k,
                                     const int32_t* route_row, const float* topk_w, int type,
