@@ -68,7 +68,9 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
   fp8_lds_t* const lds_base = (fp8_lds_t*)lds;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int wm = wave % WM, wn = wave / WM;
+  // Wavefronts of the same tokens side by side: they are on different SIMDs, and of 8 the second four
+  // have the tile's second half of tokens, so a tile of half its rows leaves no SIMD idle (below).
+  const int wm = wave / WN, wn = wave % WN;
   const int r = lane & 15, g = lane >> 4;
   const int KB = (p.K + kScaleBlock - 1) / kScaleBlock;
   const int k_end = min(p.K, t.s1 * kScaleBlock);
@@ -327,6 +329,33 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
   constexpr int kBehind = JA < JB ? PA : 0;   // loads behind those that JB waits for
   // 64 stages at a time: the scales' register is loaded between them only, else the compiler
   // would wait for all loads in every stage before it reads a lane of it.
+  if (16 * MI * wm >= rows_a) {
+    // A wavefront without rows only loads its share: the matrix unit is left to the others.
+    for (int s = t.s0; s < t.s1; ++s) {
+      const int next = buf + 1 == NBUF ? 0 : buf + 1;
+      cut_off(s + NBUF);
+      if constexpr (JA < JB) {
+        asm volatile("s_barrier" ::: "memory");
+        more_scales(s, s - t.s0);
+#pragma unroll
+        for (int q = 0; q < PA; ++q) issue_a(q, s + NBUF, buf);
+      }
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NBUF - 2) * (PA + PB) + kBehind)
+                   : "memory");
+      asm volatile("s_barrier" ::: "memory");
+      if constexpr (JA == JB) {
+        more_scales(s, s - t.s0);
+#pragma unroll
+        for (int q = 0; q < PA; ++q) issue_a(q, s + NBUF, buf);
+      }
+#pragma unroll
+      for (int q = 0; q < PB; ++q) issue_b(q, s + NBUF, buf);
+      next_place();
+      buf = next;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    return;
+  }
   for (int c0 = t.s0; c0 < t.s1; c0 += 64) {
     if (c0 > t.s0) load_sb(c0);
 #pragma unroll
