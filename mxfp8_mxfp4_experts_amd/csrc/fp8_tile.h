@@ -4,19 +4,29 @@
 // 16 MI WM x 16 NI WN tile, each wavefront MI x NI accumulators of 16x16.  K advances in stages
 // of 128 bytes per row: one cache line, one scale block, one v_mfma_f32_16x16x128_f8f6f4 per
 // accumulator, which starts from zero; the vector unit adds its result times the block's scale
-// to the running sum, while the matrix unit works on the next column of accumulators.  The
-// sums are vector registers, so a wavefront has at most MI * NI = 28 of them, and two
-// wavefronts share a SIMD.
+// to the running sum, while the matrix unit works on the next column of accumulators.  Such a
+// product takes the matrix unit 32 clocks and an issue slot of the vector unit half of that; its
+// four multiply-adds just fit beside it, each further vector instruction costs 4 clocks.  So the
+// sums are vector registers (to move them costs more than to add), and a wavefront has at most
+// MI * NI = 32 of them, two wavefronts to a SIMD.
 //
-// Stages come by direct global-to-LDS loads into a ring of NBUF, the tokens' scales with them
-// (4 bytes per token, ordered so that a lane reads its MI scales at once); the weight's scales
-// of 64 stages sit in one register, a lane each.  One barrier per stage, before the last
-// column's products: by then all of this stage is in registers, its buffer is free, and the next
-// stage's first operands are read behind these products.
+// Stages come by direct global-to-LDS loads into a ring of NBUF, the tokens' scales in a ring of
+// their own, four stages at a time (4 bytes per token, ordered so that a lane reads its MI scales
+// at once); the weight's scales of 64 stages sit in one register, a lane each.  From there a
+// small tile's operands go to registers a whole stage ahead of their products (kFull), a large
+// tile's column by column, with a barrier where the tokens' and where the weights' buffer is read
+// to its end: it is loaded anew from there on.
 //
 // LDS rows are 128 bytes with their 16-byte chunks XOR-swizzled by the row's low three bits.
 // Rows past the tile's last, chunks past K and stages past the last are loads beyond the buffer's
 // end: they bring zeros and touch no memory.
+//
+// What bounds it: 8192 x 3584 x 7168 in 256 x 256 tiles 172 .. 180 us, 2.4 POP/s, the matrix unit
+// (219 us with 128 x 128 tiles, 330 with 64 x 64); 256 x 3584 x 7168 in 64 x 64 tiles 17 us, 205 MB
+// from the L2s to the CUs at 60 .. 70 bytes/ns per CU (18.9 with 64 x 128 tiles and K in two).
+// Deeper rings, two stages per barrier, weights laid out by K and prefetches into L2 gained
+// nothing; with 224 columns a tile, a wavefront's columns meet two scales and each product needs
+// a multiplication more, which took what the better fit of 3584 columns gave.
 #pragma once
 
 #include "fp8.h"
@@ -68,8 +78,8 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
   fp8_lds_t* const lds_base = (fp8_lds_t*)lds;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  // Wavefronts of the same tokens side by side: they are on different SIMDs, and of 8 the second four
-  // have the tile's second half of tokens, so a tile of half its rows leaves no SIMD idle (below).
+  // Wavefronts of the same tokens side by side: they are on different SIMDs, and of 8 the second
+  // four have the tile's second half of tokens, so a tile of half its rows leaves no SIMD idle.
   const int wm = wave / WN, wn = wave % WN;
   const int r = lane & 15, g = lane >> 4;
   const int KB = (p.K + kScaleBlock - 1) / kScaleBlock;
@@ -156,7 +166,8 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
   auto load_sb = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
     for (int x = 0; x < NX; ++x)
-      vsb[x] = p.sb[((int64_t)t.expert * n_blocks + min(n_wave / kScaleBlock + x, n_blocks - 1)) * KB +
+      vsb[x] = p.sb[((int64_t)t.expert * n_blocks +
+                     min(n_wave / kScaleBlock + x, n_blocks - 1)) * KB +
                     min(s + lane, KB - 1)];
   };
   load_sb(t.s0);
@@ -307,146 +318,147 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
       if (n & 1) step(c0 + n - 1, n - 1, one, two);   // the last of all: 64 is even
     }
   } else {
-  // Weight operands in registers: the current column's and the next two, in a ring that comes out
-  // even with the columns where that costs no more registers.
-  constexpr int F = NI % 4 == 0 ? 4 : 3;
-  Op fa[MI], fb[F];
-  float fs[MI];                     // the tokens' scales
-  {
-    const fp8_lds_t *A = at_lds(0), *B = at_lds(0);
-    fb[0] = read_b(B, 0);
+    // Weight operands in registers: the current column's and the next two, in a ring that comes out
+    // even with the columns where that costs no more registers.
+    constexpr int F = NI % 4 == 0 ? 4 : 3;
+    Op fa[MI], fb[F];
+    float fs[MI];                     // the tokens' scales
+    {
+      const fp8_lds_t *A = at_lds(0), *B = at_lds(0);
+      fb[0] = read_b(B, 0);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) fa[i] = read_a(A, i);
-    read_s(at_lds(0), fs);
-  }
-  // Barrier JB is before the last two columns: by then their operands are in registers, so this
-  // stage's weights are no longer needed in LDS, and the next stage is complete.  The tokens'
-  // operands are in registers from the stage's start, so where there are columns enough a barrier
-  // of their own, JA, frees the tokens' buffer almost a stage earlier: their loads and the
-  // weights' then take turns, and each has about a stage's time to come.
-  constexpr int JB = NI > 2 ? NI - 2 : NI - 1;
-  constexpr int JA = NI == 8 ? 1 : JB;
-  constexpr int kBehind = JA < JB ? PA : 0;   // loads behind those that JB waits for
-  // 64 stages at a time: the scales' register is loaded between them only, else the compiler
-  // would wait for all loads in every stage before it reads a lane of it.
-  if (16 * MI * wm >= rows_a) {
-    // A wavefront without rows only loads its share: the matrix unit is left to the others.
-    for (int s = t.s0; s < t.s1; ++s) {
-      const int next = buf + 1 == NBUF ? 0 : buf + 1;
-      cut_off(s + NBUF);
-      if constexpr (JA < JB) {
-        asm volatile("s_barrier" ::: "memory");
-        more_scales(s, s - t.s0);
-#pragma unroll
-        for (int q = 0; q < PA; ++q) issue_a(q, s + NBUF, buf);
-      }
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NBUF - 2) * (PA + PB) + kBehind)
-                   : "memory");
-      asm volatile("s_barrier" ::: "memory");
-      if constexpr (JA == JB) {
-        more_scales(s, s - t.s0);
-#pragma unroll
-        for (int q = 0; q < PA; ++q) issue_a(q, s + NBUF, buf);
-      }
-#pragma unroll
-      for (int q = 0; q < PB; ++q) issue_b(q, s + NBUF, buf);
-      next_place();
-      buf = next;
+      for (int i = 0; i < MI; ++i) fa[i] = read_a(A, i);
+      read_s(at_lds(0), fs);
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    return;
-  }
-  for (int c0 = t.s0; c0 < t.s1; c0 += 64) {
-    if (c0 > t.s0) load_sb(c0);
-#pragma unroll
-    for (int x = 0; x < NX; ++x) asm volatile("" : "+v"(vsb[x]));
-    const int c1 = min(t.s1, c0 + 64);
-#pragma unroll 1
-    for (int s = c0; s < c1; ++s) {
-      float sb[NX];
-#pragma unroll
-      for (int x = 0; x < NX; ++x)
-        sb[x] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vsb[x]), s - c0));
-      const int next = buf + 1 == NBUF ? 0 : buf + 1;
-      const fp8_lds_t* B = at_lds(buf * G::kStageB);
-      const fp8_lds_t* A1 = at_lds(next * G::kStageA);
-      const fp8_lds_t* B1 = at_lds(next * G::kStageB);
-      cut_off(s + NBUF);
-      if (NI > 1) fb[1] = read_b(B, 1);
-#pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        if (j == JA && JA < JB) {
-#pragma unroll
-          for (int q = 0; q < JA * MI; ++q) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
-          }
-          __builtin_amdgcn_sched_barrier(0);
+    // Barrier JB is before the last two columns: by then their operands are in registers, so this
+    // stage's weights are no longer needed in LDS, and the next stage is complete.  The tokens'
+    // operands are in registers from the stage's start, so where there are columns enough a barrier
+    // of their own, JA, frees the tokens' buffer almost a stage earlier: their loads and the
+    // weights' then take turns, and each has about a stage's time to come.
+    constexpr int JB = NI > 2 ? NI - 2 : NI - 1;
+    constexpr int JA = NI == 8 ? 1 : JB;
+    constexpr int kBehind = JA < JB ? PA : 0;   // loads behind those that JB waits for
+    if (16 * MI * wm >= rows_a) {
+      // A wavefront without rows only loads its share: the matrix unit is left to the others.
+      // (16384 x 3584 x 3584 in 28 experts, 585 rows each: 255 -> 241 us.)
+      for (int s = t.s0; s < t.s1; ++s) {
+        const int next = buf + 1 == NBUF ? 0 : buf + 1;
+        cut_off(s + NBUF);
+        if constexpr (JA < JB) {
           asm volatile("s_barrier" ::: "memory");
-          more_scales(s, s - c0);
+          more_scales(s, s - t.s0);
 #pragma unroll
           for (int q = 0; q < PA; ++q) issue_a(q, s + NBUF, buf);
         }
-        if (j == JB) {
-          // So far: a share of the loads, the LDS reads and the sums behind every product.
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NBUF - 2) * (PA + PB) + kBehind)
+                     : "memory");
+        asm volatile("s_barrier" ::: "memory");
+        if constexpr (JA == JB) {
+          more_scales(s, s - t.s0);
 #pragma unroll
-          for (int q = 0; q < (JA < JB ? JB - JA : JB) * MI; ++q) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, MI == 1 ? 2 : 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NBUF - 2) * (PA + PB) + kBehind)
-                       : "memory");
-          asm volatile("s_barrier" ::: "memory");
-          if constexpr (JA == JB) {
+          for (int q = 0; q < PA; ++q) issue_a(q, s + NBUF, buf);
+        }
+#pragma unroll
+        for (int q = 0; q < PB; ++q) issue_b(q, s + NBUF, buf);
+        next_place();
+        buf = next;
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      return;
+    }
+    // 64 stages at a time: the scales' register is loaded between them only, else the compiler
+    // would wait for all loads in every stage before it reads a lane of it.
+    for (int c0 = t.s0; c0 < t.s1; c0 += 64) {
+      if (c0 > t.s0) load_sb(c0);
+#pragma unroll
+      for (int x = 0; x < NX; ++x) asm volatile("" : "+v"(vsb[x]));
+      const int c1 = min(t.s1, c0 + 64);
+#pragma unroll 1
+      for (int s = c0; s < c1; ++s) {
+        float sb[NX];
+#pragma unroll
+        for (int x = 0; x < NX; ++x)
+          sb[x] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vsb[x]), s - c0));
+        const int next = buf + 1 == NBUF ? 0 : buf + 1;
+        const fp8_lds_t* B = at_lds(buf * G::kStageB);
+        const fp8_lds_t* A1 = at_lds(next * G::kStageA);
+        const fp8_lds_t* B1 = at_lds(next * G::kStageB);
+        cut_off(s + NBUF);
+        if (NI > 1) fb[1] = read_b(B, 1);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          if (j == JA && JA < JB) {
+#pragma unroll
+            for (int q = 0; q < JA * MI; ++q) {
+              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_barrier" ::: "memory");
             more_scales(s, s - c0);
 #pragma unroll
             for (int q = 0; q < PA; ++q) issue_a(q, s + NBUF, buf);
           }
+          if (j == JB) {
+            // So far: a share of the loads, the LDS reads and the sums behind every product.
 #pragma unroll
-          for (int q = 0; q < PB; ++q) issue_b(q, s + NBUF, buf);
+            for (int q = 0; q < (JA < JB ? JB - JA : JB) * MI; ++q) {
+              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x100, MI == 1 ? 2 : 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NBUF - 2) * (PA + PB) + kBehind)
+                         : "memory");
+            asm volatile("s_barrier" ::: "memory");
+            if constexpr (JA == JB) {
+              more_scales(s, s - c0);
+#pragma unroll
+              for (int q = 0; q < PA; ++q) issue_a(q, s + NBUF, buf);
+            }
+#pragma unroll
+            for (int q = 0; q < PB; ++q) issue_b(q, s + NBUF, buf);
+          }
+          // Column j + 2's operand, or the next stage's first.
+          if (j + 2 < NI)
+            fb[(j + 2) % F] = read_b(B, j + 2);
+          else if (j == NI - 1)
+            fb[NI % F] = read_b(B1, 0);
+          float sj = sb[0];
+          if constexpr (NX == 2)
+            sj = (n_wave + 16 * j) / kScaleBlock == n_wave / kScaleBlock ? sb[0] : sb[1];
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            add(i, (j + NI - 1) % NI);
+            if (NX == 2 || j == 0) f[i] = fs[i] * sj;
+            prod[i] = mfma_fp8(fb[j % F].lo, fb[j % F].hi, fa[i].lo, fa[i].hi);
+            if (j == NI - 1) fa[i] = read_a(A1, i);
+          }
         }
-        // Column j + 2's operand, or the next stage's first.
-        if (j + 2 < NI)
-          fb[(j + 2) % F] = read_b(B, j + 2);
-        else if (j == NI - 1)
-          fb[NI % F] = read_b(B1, 0);
-        float sj = sb[0];
-        if constexpr (NX == 2)
-          sj = (n_wave + 16 * j) / kScaleBlock == n_wave / kScaleBlock ? sb[0] : sb[1];
+        next_place();
+        read_s(at_lds(place * BM * 4), fs);
+        // From the barrier on: the loads too.
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          add(i, (j + NI - 1) % NI);
-          if (NX == 2 || j == 0) f[i] = fs[i] * sj;
-          prod[i] = mfma_fp8(fb[j % F].lo, fb[j % F].hi, fa[i].lo, fa[i].hi);
-          if (j == NI - 1) fa[i] = read_a(A1, i);
+        for (int q = 0; q < (NI - JB - 1) * MI; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
         }
-      }
-      next_place();
-      read_s(at_lds(place * BM * 4), fs);
-      // From the barrier on: the loads too.
 #pragma unroll
-      for (int q = 0; q < (NI - JB - 1) * MI; ++q) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+        for (int q = 0; q < MI; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+        }
+        if constexpr (NI % F != 0) fb[0] = fb[NI % F];
+        asm volatile("" ::: "memory");
+        buf = next;
       }
-#pragma unroll
-      for (int q = 0; q < MI; ++q) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
-      }
-      if constexpr (NI % F != 0) fb[0] = fb[NI % F];
-      asm volatile("" ::: "memory");
-      buf = next;
     }
-  }
   }
 #pragma unroll
   for (int i = 0; i < MI; ++i) add(i, NI - 1);
@@ -590,7 +602,9 @@ __device__ __forceinline__ Fp8Place fp8_find(const Fp8Params& p, int per, int ow
 // own, or that there is none left for it.  Each XCD takes a contiguous range of the tiles, an
 // expert's column by column, so that what runs at once on an XCD shares weights and tokens.
 // (Workgroups that stay and take tile after tile were slower: 16384 x 3584 x 3584 in 32 experts
-// 316 us, see below: nothing covers a tile's first loads and its stores.)
+// 316 us against 278: nothing covers a tile's first loads and its stores.  All experts' whole tiles
+// first and the last, shorter ones of each after them: in 28 experts 269 against 241, since an
+// expert's tiles then no longer share its weights.)
 template <int WM, int WN, int MI, int NI, int NBUF, int WPE>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE)))
 void fp8_grouped_kernel(Fp8Params p, Fp8Cut cut) {
