@@ -490,23 +490,49 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
       return make_uint2(f32x2_to_bf16x2(acc[i][j][0], acc[i][j][1]),
                         f32x2_to_bf16x2(acc[i][j][2], acc[i][j][3]));
     };
+    static_assert(NI % 2 == 0, "columns in pairs of blocks");
+    auto pieces = [&](int i, int j) __attribute__((always_inline)) {
+      const uint2 u = pack(i, j), v = pack(i, j + 1);
+      const auto x = __builtin_amdgcn_permlane16_swap(u.x, v.x, false, false);
+      const auto y = __builtin_amdgcn_permlane16_swap(u.y, v.y, false, false);
+      return any4{x[0], y[0], x[1], y[1]};
+    };
     uint16_t* o2 = p.out + m_w * p.ld_out + n_wave + 16 * (g & 1) + 8 * (g >> 1);
+    const uint32_t first = (uint32_t)(reinterpret_cast<uintptr_t>(p.out) >> 1);
+    if (((first | (uint32_t)p.ld_out) & 1) == 0) {
 #pragma unroll
-    for (int j = 0; j + 1 < NI; j += 2)
+      for (int j = 0; j < NI; j += 2)
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const uint2 u = pack(i, j), v = pack(i, j + 1);
-        const auto x = __builtin_amdgcn_permlane16_swap(u.x, v.x, false, false);
-        const auto y = __builtin_amdgcn_permlane16_swap(u.y, v.y, false, false);
-        if (m_w + 16 * i < t.m1)
-          *reinterpret_cast<any4*>(o2 + 16 * i * p.ld_out + 16 * j) = any4{x[0], y[0], x[1], y[1]};
-      }
-    if constexpr (NI % 2 == 1) {
-      uint16_t* o = p.out + m_w * p.ld_out + n_w + 16 * (NI - 1);
+        for (int i = 0; i < MI; ++i) {
+          const any4 v = pieces(i, j);
+          if (m_w + 16 * i < t.m1) *reinterpret_cast<any4*>(o2 + 16 * i * p.ld_out + 16 * j) = v;
+        }
+      return;
+    }
+    // Rows may start between two dwords, where a 16-byte store takes several times as long (8192 x
+    // 3585 x 1024: 60 us instead of 41).  There a lane stores the 8 columns from its second on, the
+    // last of them from the lane with the columns after its own; the row's first column is stored
+    // by itself, and the last lane stores its columns where they are.
+    const int after = r + 16 * (g == 0 ? 2 : g == 2 ? 1 : g == 1 ? 3 : 0);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const uint2 u = pack(i, NI - 1);
-        if (m_w + 16 * i < t.m1) *reinterpret_cast<any2*>(o + 16 * i * p.ld_out) = any2{u.x, u.y};
+    for (int i = 0; i < MI; ++i) {
+      const bool odd = ((first + (uint32_t)(m_w + 16 * i) * (uint32_t)p.ld_out) & 1) != 0;
+      any4 v = pieces(i, 0);
+#pragma unroll
+      for (int j = 0; j < NI; j += 2) {
+        any4 next = v;
+        if (j + 2 < NI) next = pieces(i, j + 2);
+        const uint32_t more = (uint32_t)__shfl((int)(g == 0 ? next[0] : v[0]), after);
+        const bool shift = odd && (g != 3 || j + 2 < NI);
+        uint16_t* o = o2 + 16 * i * p.ld_out + 16 * j;
+        if (m_w + 16 * i < t.m1) {
+          if (odd && g == 0 && j == 0) *o = (uint16_t)v[0];
+          if (shift)
+            v = any4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16,
+                     v[3] >> 16 | more << 16};
+          *reinterpret_cast<any4*>(o + shift) = v;
+        }
+        v = next;
       }
     }
     return;

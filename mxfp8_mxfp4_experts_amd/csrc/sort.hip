@@ -10,9 +10,9 @@
 // read or written once and what they differ in moves as whole rows; nothing is added with
 // atomics, and equal calls give equal bits.
 //
-// Memory bounds them at many tokens: 4096 tokens x 8 routes x 3584 in bf16, sort 264 MB in 45 us, 5.9
-// TB/s; unsort 50 us, 5.3; gradients 499 MB in 90 us, 5.5 (a copy of 2 GiB reaches 5.0).  That takes
-// loads and stores that leave the caches alone (NT): with plain ones 51, 56 and 99 us.  Rows that
+// Memory bounds them at many tokens: 4096 tokens x 8 routes x 3584 in bf16, sort 264 MB in 45 us,
+// 5.9 TB/s; unsort 50 us, 5.3; gradients 499 MB in 90 us, 5.5 (a copy of 2 GiB reaches 5.0).  That
+// takes loads and stores that leave the caches alone (NT): with plain ones 51, 56 and 99 us.  Rows that
 // the caches hold for what comes next, or from what came before, are left in them: 256 tokens x 8
 // (15 MB) unsort 5.9 us plain and 7.2 past the caches.  At few tokens the chain of place, load and
 // store bounds them: 8 x 16 x 7168 sort 3.6 us, unsort 5.0.
@@ -250,6 +250,10 @@ bool grid_of(int64_t blocks, dim3& grid) {
 // MB: 25.9 us with plain loads and stores, 24.4 past the caches; unsort 12.7 and 12.7; of 2048, 117
 // MB: 51.7 and 47.0; 30.2 and 25.6.)
 constexpr int64_t kCached = 64 << 20;
+// Sorted rows that begin or end within 64 bytes go through the caches all the same: 4096 x 8 x 3592
+// in bf16 take 43 us so and 67 past them where the memory-side cache still holds the rows, 65 and
+// 69 where not (3616 columns 44 .. 49 and 52, 58 and 52).
+constexpr int kHalfLine = 64;
 // Slots of a token that one unit of the gradients takes: with 8 instead of 4, 8 tokens x 16 slots
 // take 8.5 us instead of 5.9 and 4096 x 8 93 instead of 90.
 constexpr int kGradSlots = 4;
@@ -284,8 +288,11 @@ hipError_t sort_launch(const SortParams& p, SortOp op, hipStream_t stream) {
 template <class T, int V>
 hipError_t sort_launch(const SortParams& p, SortOp op, hipStream_t stream) {
   const int64_t rows = (int64_t)p.T * p.top_k < p.n_rows ? (int64_t)p.T * p.top_k : p.n_rows;
-  return rows * p.H * (int64_t)sizeof(T) > kCached ? sort_launch<T, V, true>(p, op, stream)
-                                                   : sort_launch<T, V, false>(p, op, stream);
+  const uint64_t bytes = (uint64_t)(p.ld_rows | p.H) * sizeof(T);
+  const bool odd = op == SortOp::kSort &&
+                   (bytes | reinterpret_cast<uintptr_t>(p.rows)) % kHalfLine != 0;
+  return rows * p.H * (int64_t)sizeof(T) > kCached && !odd ? sort_launch<T, V, true>(p, op, stream)
+                                                           : sort_launch<T, V, false>(p, op, stream);
 }
 
 }  // namespace
