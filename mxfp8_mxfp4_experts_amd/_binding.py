@@ -58,6 +58,10 @@ _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
 
+_CALLS = ("quant_fp8", "fp8_matmul", "fp8_linear", "fp8_grouped", "sort_tokens", "unsort_tokens",
+          "unsort_tokens_grad", "permute")
+
+
 def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(
@@ -135,6 +139,8 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.moe_unsort_tokens_grad.restype = _I
     lib.moe_unsort_tokens_grad.argtypes = [_P, _I64, _P, _I64, _I, _I, _I, _I, _P, _P, _I, _P,
                                            _I64, _P, _P]
+    # Where the compiled helper finds the calls that it makes itself.
+    lib.at = {name: ctypes.cast(getattr(lib, "moe_" + name), _P).value for name in _CALLS}
     return lib
 
 
@@ -293,21 +299,14 @@ def moe_route_quant_permute(logits: torch.Tensor, bias: Optional[torch.Tensor], 
 
 def moe_permute(topk_idx: torch.Tensor, expert_offset: int, E_local: int, workspace: torch.Tensor,
                 expert_offsets=None, sorted_route=None, route_row=None):
-    # In front of copies of a few microseconds the checks count: one look at each tensor, and what
-    # is wrong, or only out of the ordinary, is found below.
-    head = _head(topk_idx)
-    if (head is not None and expert_offsets is not None and sorted_route is not None and
-            route_row is not None):
-        idx, T, K = head
-        ptrs = (_plain(topk_idx, torch.int32, T, K, idx),
-                _plain(expert_offsets, torch.int32, E_local + 1, -1, idx),
-                _plain(sorted_route, torch.int32, T * K, -1, idx),
-                _plain(route_row, torch.int32, T * K, -1, idx))
-        if min(ptrs) >= 0:
-            _need(workspace, "workspace", torch.uint8, device=topk_idx.device)
-            _check("moe_permute", (_lib or lib()).moe_permute(
-                ptrs[0], T, K, expert_offset, E_local, *ptrs[1:], workspace.data_ptr(),
-                workspace.numel(), _raw_stream(idx)))
+    # In front of copies of a few microseconds the checks count: with every buffer given and right
+    # they are made in the helper.
+    if expert_offsets is not None and sorted_route is not None and route_row is not None:
+        st = _call.permute((_lib or lib()).at["permute"], _raw_stream, topk_idx, expert_offset,
+                           E_local, workspace, expert_offsets, sorted_route, route_row)
+        if st is not None:
+            if st:
+                raise MoEError("moe_permute", st)
             return expert_offsets, sorted_route, route_row
     _need(topk_idx, "topk_idx", torch.int32)
     if topk_idx.dim() != 2:
@@ -525,6 +524,20 @@ def _load_args():
         raise ImportError("_tensor_args.so is missing or does not fit this torch: build it with "
                           "`python -m mxfp8_mxfp4_experts_amd.build`") from e
     _head, _plain = _tensor_args.head, _tensor_args.plain
+
+
+class _Calls:
+    """The helper's check-and-call functions, found on first use: the status
+    of a call whose buffers are all given and plainly right, else None."""
+
+    def __getattr__(self, name):
+        from . import _tensor_args
+        _load_args()
+        setattr(self, name, getattr(_tensor_args, name))
+        return getattr(self, name)
+
+
+_call = _Calls()
 
 
 def _head(x):
@@ -880,6 +893,12 @@ def _bf16_out(out, rows, cols, idx):
 def moe_quant_fp8(x, xq=None, xs=None):
     """bf16 rows [T, H] -> E4M3 codes uint8 [T, H] and float scales
     [ceil(H / 128), T], one for each row and 128 elements."""
+    if xq is not None and xs is not None:
+        st = _call.quant_fp8((_lib or lib()).at["quant_fp8"], _raw_stream, x, xq, xs)
+        if st is not None:
+            if st:
+                raise MoEError("moe_quant_fp8", st)
+            return xq, xs
     head = _head(x)
     if head is None:
         _no_head(x, "x")
@@ -921,6 +940,13 @@ def moe_fp8_matmul_workspace_size(M: int, N: int, K: int) -> int:
 def moe_fp8_matmul(xq, xs, w, w_s, out=None, workspace=None):
     """out bf16 [M, N] = xq [M, K] . w [N, K], both E4M3, scaled block by block:
     xs float [ceil(K / 128), M], w_s float [ceil(N / 128), ceil(K / 128)]."""
+    if out is not None and workspace is not None:
+        st = _call.fp8_matmul((_lib or lib()).at["fp8_matmul"], _raw_stream, xq, xs, w, w_s, out,
+                              workspace)
+        if st is not None:
+            if st:
+                raise MoEError("moe_fp8_matmul", st)
+            return out
     head = _head(xq)
     if head is None:
         _no_head(xq, "xq")
@@ -940,6 +966,13 @@ def moe_fp8_matmul(xq, xs, w, w_s, out=None, workspace=None):
 
 def moe_fp8_linear(x, w, w_s, out=None, workspace=None):
     """moe_quant_fp8 of x [M, K] (bf16) and moe_fp8_matmul as one call."""
+    if out is not None and workspace is not None:
+        st = _call.fp8_linear((_lib or lib()).at["fp8_linear"], _raw_stream, x, w, w_s, out,
+                              workspace)
+        if st is not None:
+            if st:
+                raise MoEError("moe_fp8_linear", st)
+            return out
     head = _head(x)
     if head is None:
         _no_head(x, "x")
@@ -965,6 +998,13 @@ def moe_fp8_grouped(xq, xs, w, w_s, expert_offsets, sorted_route=None, top_k: in
     is xq[sorted_route[j] / top_k], without it xq stands in expert order.  Rows
     behind the last expert's are left as they were (a new ``out`` holds anything
     there)."""
+    if out is not None:
+        st = _call.fp8_grouped((_lib or lib()).at["fp8_grouped"], _raw_stream, xq, xs, w, w_s,
+                               expert_offsets, sorted_route, top_k, out)
+        if st is not None:
+            if st:
+                raise MoEError("moe_fp8_grouped", st)
+            return out
     head = _head(xq)
     if head is None:
         _no_head(xq, "xq")
@@ -1041,6 +1081,13 @@ def moe_sort_tokens(x, route_row, top_k: int, rows=None):
     float32, route_row int32 [T * top_k] of moe_permute, rows [n, H] (n = T *
     top_k where not given, and rows that no route has hold anything then).  Its
     gradient is ``moe_unsort_tokens(drows, route_row, None, top_k)``."""
+    if rows is not None:
+        st = _call.sort_tokens((_lib or lib()).at["sort_tokens"], _raw_stream, x, route_row, top_k,
+                               rows)
+        if st is not None:
+            if st:
+                raise MoEError("moe_sort_tokens", st)
+            return rows
     head = _head(x)
     if head is None:
         _no_head(x, "x")
@@ -1063,6 +1110,13 @@ def moe_unsort_tokens(rows, route_row, topk_w, top_k: int, out=None):
     """out[t] = sum over kept k of topk_w[t, k] * rows[route_row[t, k]]: rows
     [n, H] bf16 or float32, topk_w float [T, top_k] or None (the plain sum),
     out [T, H] of the rows' type."""
+    if out is not None:
+        st = _call.unsort_tokens((_lib or lib()).at["unsort_tokens"], _raw_stream, rows, route_row,
+                                 topk_w, top_k, out)
+        if st is not None:
+            if st:
+                raise MoEError("moe_unsort_tokens", st)
+            return out
     head = _head(rows)
     if head is None:
         _no_head(rows, "rows")
@@ -1093,6 +1147,13 @@ def moe_unsort_tokens_grad(dout, rows, route_row, topk_w, drows=None, dw=None,
     were; a new ``drows`` holds anything there) and dw float [T, top_k], dw[t, k]
     = <dout[t], rows[route_row[t, k]]>.  ``want_drows`` / ``want_dw`` False
     leaves one out (None) where no buffer is given."""
+    if drows is not None and dw is not None:
+        st = _call.unsort_tokens_grad((_lib or lib()).at["unsort_tokens_grad"], _raw_stream, dout,
+                                      rows, route_row, topk_w, drows, dw)
+        if st is not None:
+            if st:
+                raise MoEError("moe_unsort_tokens_grad", st)
+            return drows, dw
     head = _head(dout)
     if head is None:
         _no_head(dout, "dout")

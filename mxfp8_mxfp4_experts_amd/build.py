@@ -83,6 +83,8 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
 
 ARGS_SRC = os.path.join(PKG, "csrc_py", "tensor_args.cpp")
 ARGS_OUT = os.path.join(PKG, "_tensor_args.so")
+# hip_runtime_api.h, which the C header includes for its stream type.
+ROCM_INCLUDE = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")
 
 
 def build_args(verbose: bool = False) -> str:
@@ -97,7 +99,7 @@ def build_args(verbose: bool = False) -> str:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = ARGS_OUT + ".tmp"
     rc, out = _run([HIPCC, "-x", "c++", "-no-hip-rt", "-O2", "-std=c++17", "-shared", "-fPIC",
-                    "-Wall",
+                    "-Wall", "-D__HIP_PLATFORM_AMD__", "-isystem", ROCM_INCLUDE,
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
                     "-I", sysconfig.get_paths()["include"], "-isystem", inc, "-isystem",
                     os.path.join(inc, "torch", "csrc", "api", "include"), ARGS_SRC, "-L", libs,
