@@ -480,7 +480,7 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
       }
     return;
   }
-  // Rows start at any element (8- and 16-byte stores at element alignment).
+  // Rows may start at any element: 8- and 16-byte stores at element alignment.
   typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
   typedef uint32_t any2 __attribute__((ext_vector_type(2), aligned(2)));
   if (t.n0 + BN <= p.N) {
@@ -498,8 +498,7 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
       return any4{x[0], y[0], x[1], y[1]};
     };
     uint16_t* o2 = p.out + m_w * p.ld_out + n_wave + 16 * (g & 1) + 8 * (g >> 1);
-    const uint32_t first = (uint32_t)(reinterpret_cast<uintptr_t>(p.out) >> 1);
-    if (((first | (uint32_t)p.ld_out) & 1) == 0) {
+    if ((p.ld_out & 1) == 0) {
 #pragma unroll
       for (int j = 0; j < NI; j += 2)
 #pragma unroll
@@ -509,14 +508,14 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
         }
       return;
     }
-    // Rows may start between two dwords, where a 16-byte store takes several times as long (8192 x
-    // 3585 x 1024: 60 us instead of 41).  There a lane stores the 8 columns from its second on, the
-    // last of them from the lane with the columns after its own; the row's first column is stored
-    // by itself, and the last lane stores its columns where they are.
+    // Every other row starts between two dwords (the first one on 16 bytes), where a 16-byte store
+    // takes several times as long (8192 x 3585 x 1024: 60 us instead of 41).  There a lane stores
+    // the 8 columns from its second on, the last of them from the lane with the columns after its
+    // own; the first column is stored by itself, and the last lane's columns where they are.
+    const bool odd = (m_w & 1) != 0;
     const int after = r + 16 * (g == 0 ? 2 : g == 2 ? 1 : g == 1 ? 3 : 0);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const bool odd = ((first + (uint32_t)(m_w + 16 * i) * (uint32_t)p.ld_out) & 1) != 0;
       any4 v = pieces(i, 0);
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
