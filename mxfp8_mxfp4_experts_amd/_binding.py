@@ -531,8 +531,8 @@ class _Calls:
     of a call whose buffers are all given and plainly right, else None."""
 
     def __getattr__(self, name):
-        from . import _tensor_args
         _load_args()
+        from . import _tensor_args
         setattr(self, name, getattr(_tensor_args, name))
         return getattr(self, name)
 
