@@ -586,18 +586,14 @@ void fp8_tile_kernel(Fp8Params p, Fp8Cut cut) {
       lds);
 }
 
-// The expert of the tile of rows with number `slot`, tiles of BM rows counted expert by expert, and
-// the number of tiles before that expert.  A wavefront's lanes
-// each count a run of experts, then the run with the tile is looked at expert by expert: two loads
-// one after the other (one up to 64 experts).  Offsets out of order count as empty experts.
-struct Fp8Place {
-  int expert, before;
+// The output rows of an expert.  Offsets out of order are an empty expert.
+struct Fp8Span {
+  int first, end;
 };
-template <int BM>
-__device__ __forceinline__ int fp8_tiles_of(const Fp8Params& p, int e) {
-  if (e >= p.E) return 0;
-  const int a = max(p.offs[e], 0), b = min(p.offs[e + 1], p.M);
-  return b > a ? (b - a + BM - 1) / BM : 0;
+__device__ __forceinline__ Fp8Span fp8_span(const Fp8Params& p, int e) {
+  if (e >= p.E) return {0, 0};
+  const int first = max(p.offs[e], 0);
+  return {first, max(min(p.offs[e + 1], p.M), first)};
 }
 __device__ __forceinline__ int fp8_wave_scan(int v) {   // inclusive
   const int lane = threadIdx.x & 63;
@@ -607,20 +603,6 @@ __device__ __forceinline__ int fp8_wave_scan(int v) {   // inclusive
     if (lane >= d) v += y;
   }
   return v;
-}
-template <int BM>
-__device__ __forceinline__ Fp8Place fp8_find(const Fp8Params& p, int per, int own, int sum,
-                                             int slot) {
-  const int lane = threadIdx.x & 63;
-  const uint64_t past = __ballot(sum > slot);
-  const int l = __ffsll((long long)past) - 1;      // the run with the tile
-  int before = __shfl(sum - own, l);
-  if (per == 1) return {l, before};
-  const int mine = lane < per ? fp8_tiles_of<BM>(p, l * per + lane) : 0;
-  const int upto = before + fp8_wave_scan(mine);
-  const int k = __ffsll((long long)__ballot(upto > slot)) - 1;
-  before = __shfl(upto - mine, k);
-  return {l * per + k, before};
 }
 
 // Grouped: a workgroup for every tile that there can be; it counts the experts' tiles to find its
@@ -635,25 +617,43 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WP
 void fp8_grouped_kernel(Fp8Params p, Fp8Cut cut) {
   using G = Fp8Geom<WM, WN, MI, NI, NBUF, WPE, true>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kLds];
+  // A wavefront's lanes each count the tiles of a run of experts; then the run with this workgroup's
+  // tile is looked at expert by expert (up to 64 experts: one load of offsets and no more).
   const int lane = threadIdx.x & 63, per = (p.E + 63) / 64;
-  int own = 0;
-  for (int i = 0; i < per; ++i) own += fp8_tiles_of<G::BM>(p, lane * per + i);
-  const int sum = fp8_wave_scan(own);
-  const int all = __builtin_amdgcn_readlane(sum, 63);
-  const int64_t items = (int64_t)all * cut.tiles_n;
-  const int x = blockIdx.x & 7;
-  const int64_t q = items >> 3, in_x = blockIdx.x >> 3;
+  auto tiles_of = [](Fp8Span s) { return (s.end - s.first + G::BM - 1) / G::BM; };
+  Fp8Span span = fp8_span(p, lane * per);
+  int own = tiles_of(span);
+  for (int i = 1; i < per; ++i) own += tiles_of(fp8_span(p, lane * per + i));
+  int upto = fp8_wave_scan(own);
+  // (Offsets that overlap may count more tiles than the grid has, or than 31 bits hold: what then
+  // is no tile of its expert is left out below.)
+  const uint32_t items = (uint32_t)min(
+      (int64_t)max(__builtin_amdgcn_readlane(upto, 63), 0) * cut.tiles_n, (int64_t)0x7FFFFFFF);
+  const uint32_t x = blockIdx.x & 7, q = items >> 3, in_x = blockIdx.x >> 3;
   if (in_x >= q + (x < (items & 7))) return;
-  const int64_t it = x * q + min((int64_t)x, items & 7) + in_x;
-  const Fp8Place at = fp8_find<G::BM>(p, per, own, sum, (int)(it / cut.tiles_n));
-  const int e = __builtin_amdgcn_readfirstlane(at.expert);
-  const int before = __builtin_amdgcn_readfirstlane(at.before);
-  const int tiles = fp8_tiles_of<G::BM>(p, e);
-  const int in = (int)(it - (int64_t)before * cut.tiles_n), tn = in / tiles;
-  const int64_t m0 = max(p.offs[e], 0) + (int64_t)(in - tn * tiles) * G::BM;
+  const uint32_t it = x * q + min(x, items & 7) + in_x;
+  const int slot = (int)(it / (uint32_t)cut.tiles_n);
+  int e = __ffsll((long long)__ballot(upto > slot)) - 1;
+  int before = __builtin_amdgcn_readlane(upto - own, e);
+  int at = e;                        // the lane that has the expert's rows
+  if (per > 1) {
+    span = lane < per ? fp8_span(p, e * per + lane) : Fp8Span{0, 0};
+    own = tiles_of(span);
+    upto = before + fp8_wave_scan(own);
+    at = __ffsll((long long)__ballot(upto > slot)) - 1;
+    before = __builtin_amdgcn_readlane(upto - own, at);
+    e = e * per + at;
+  }
+  const int first = __builtin_amdgcn_readlane(span.first, at);
+  const int end = __builtin_amdgcn_readlane(span.end, at);
+  const int tiles = tiles_of({first, end});
+  const uint32_t in = it - (uint32_t)before * (uint32_t)cut.tiles_n;
+  if (in >= (uint64_t)tiles * (uint32_t)cut.tiles_n) return;
+  const int tn = (int)(in / (uint32_t)tiles);
+  const int64_t m0 = first + (int64_t)((int)in - tn * tiles) * G::BM;
   fp8_tile_body<WM, WN, MI, NI, NBUF, WPE, true>(
       p, cut,
-      Fp8Tile{m0, min((int64_t)min(p.offs[e + 1], p.M), m0 + G::BM), tn * G::BN, 0,
+      Fp8Tile{m0, min((int64_t)end, m0 + G::BM), tn * G::BN, 0,
               (p.K + kScaleBlock - 1) / kScaleBlock, 0, e},
       lds);
 }
