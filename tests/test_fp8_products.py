@@ -351,6 +351,27 @@ def test_grouped_cuts_off_offsets_and_routes(m):
 
 
 @gpu
+@pytest.mark.parametrize("R,offs", [(50, [0, 40, 10, 30]), (700, [0, 600, 20, 520]),
+                                    (64, [5, 5, 3, 64]), (40, [30, 20, 10, 0])])
+def test_grouped_offsets_out_of_order(m, R, offs):
+    """An end before its start is an empty expert; rows that no expert claims are untouched, rows
+    that several claim hold, element by element, one's or what was there (such offsets may count
+    more tiles than there are rows for)."""
+    E, N, K = 3, 130, 272
+    xq, xs = m.moe_quant_fp8(ref.tokens(R, K, 1).to(DEV))
+    w, w_s = (t.to(DEV) for t in ref.weight(N, K, 2, E))
+    out = torch.full((R, N), 7.0, dtype=BF16, device=DEV)
+    m.moe_fp8_grouped(xq, xs, w, w_s, torch.tensor(offs, dtype=torch.int32, device=DEV), out=out)
+    whole = [m.moe_fp8_matmul(xq, xs, w[e], w_s[e]) for e in range(E)]
+    for j in range(R):
+        mine = [e for e in range(E) if offs[e] <= j < offs[e + 1]]
+        want = [whole[e][j] for e in mine] + [torch.full_like(out[j], 7.0)]
+        near = [torch.isclose(out[j].float(), t.float(), rtol=2 ** -6,
+                              atol=1e-3 * t.abs().max().item()) for t in want]
+        assert torch.stack(near).any(0).all(), (j, mine)
+
+
+@gpu
 @pytest.mark.parametrize("T,k", [(9, 2), (200, 2)])
 def test_grouped_strided_tokens_scales_and_output(m, T, k):
     E, N, K = 5, 130, 400
