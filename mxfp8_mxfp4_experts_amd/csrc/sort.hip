@@ -22,6 +22,7 @@
 // back to end with the row, where it repeats elements of the piece before it (the same values
 // stored twice; a sum counts them once).  Rows shorter than a piece go element by element.
 #include "common.h"
+#include "grid.h"
 #include "launch.h"
 #include "q8_dev.h"
 
@@ -241,11 +242,6 @@ __global__ __launch_bounds__(64 * kWaves) void unsort_grad_kernel(SortParams p) 
   if ((WAVE ? lane : tid) < G && k0 + lane < p.top_k) p.dw[t * p.top_k + k0 + lane] = mine;
 }
 
-bool grid_of(int64_t blocks, dim3& grid) {
-  grid = dim3((unsigned)blocks);
-  return blocks <= 0x7FFFFFFF;
-}
-
 // Rows of more bytes than this go past the caches.  (Gradients of 1024 tokens x 8 x 3584 in bf16, 59
 // MB: 25.9 us with plain loads and stores, 24.4 past the caches; unsort 12.7 and 12.7; of 2048, 117
 // MB: 51.7 and 47.0; 30.2 and 25.6.)
@@ -258,32 +254,45 @@ constexpr int kHalfLine = 64;
 // take 8.5 us instead of 5.9 and 4096 x 8 93 instead of 90.
 constexpr int kGradSlots = 4;
 
+// The tokens from t on.
+template <class T>
+void advance(SortParams& p, int64_t t) {
+  if (p.x) p.x = static_cast<T*>(p.x) + t * p.ld_x;
+  if (p.dout) p.dout = static_cast<const T*>(p.dout) + t * p.ld_dout;
+  p.route_row += t * p.top_k;
+  if (p.w) p.w += t * p.top_k;
+  if (p.dw) p.dw += t * p.top_k;
+}
+
+// More tokens than a launch takes go in several, one after another (2^26 of up to 512 elements in
+// bf16, fewer of longer ones).
 template <class T, int V, bool NT>
-hipError_t sort_launch(const SortParams& p, SortOp op, hipStream_t stream) {
-  const dim3 block(64 * kWaves);
-  dim3 grid;
+hipError_t sort_launch(SortParams p, SortOp op, hipStream_t stream) {
+  constexpr int G = kGradSlots, kThreads = 64 * kWaves;
   const int64_t pieces = (p.H + V - 1) / V;
-  if (op != SortOp::kGrad) {
-    if (!grid_of(((int64_t)p.T * ((pieces + 63) / 64) + kWaves - 1) / kWaves, grid))
-      return hipErrorInvalidConfiguration;
+  const bool grad = op == SortOp::kGrad;
+  const bool wave = pieces <= 64;   // 8192 x 2 x 512 in bf16: 9.9 us by workgroups, 5.4 so
+  const int64_t units = grad ? (p.top_k + G - 1) / G : (pieces + 63) / 64;
+  const int per_block = grad && !wave ? 1 : kWaves;
+  const int64_t most = most_items(kThreads, per_block, units);
+  for (int64_t left = p.T; left > 0; left -= p.T) {
+    p.T = (int)(left < most ? left : most);
+    const dim3 grid((unsigned)((p.T * units + per_block - 1) / per_block)), block(kThreads);
     if (op == SortOp::kSort)
       hipLaunchKernelGGL((sort_kernel<T, V, NT>), grid, block, 0, stream, p);
+    else if (grad && wave)
+      hipLaunchKernelGGL((unsort_grad_kernel<T, V, G, true, NT>), grid, block, 0, stream, p);
+    else if (grad)
+      hipLaunchKernelGGL((unsort_grad_kernel<T, V, G, false, NT>), grid, block, 0, stream, p);
     else if (p.w)
       hipLaunchKernelGGL((unsort_kernel<T, V, true, NT>), grid, block, 0, stream, p);
     else
       hipLaunchKernelGGL((unsort_kernel<T, V, false, NT>), grid, block, 0, stream, p);
-    return hipGetLastError();
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    advance<T>(p, p.T);
   }
-  constexpr int G = kGradSlots;
-  const int64_t units = (int64_t)p.T * ((p.top_k + G - 1) / G);
-  const bool wave = pieces <= 64;   // 8192 x 2 x 512 in bf16: 9.9 us by workgroups, 5.4 so
-  if (!grid_of(wave ? (units + kWaves - 1) / kWaves : units, grid))
-    return hipErrorInvalidConfiguration;
-  if (wave)
-    hipLaunchKernelGGL((unsort_grad_kernel<T, V, G, true, NT>), grid, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL((unsort_grad_kernel<T, V, G, false, NT>), grid, block, 0, stream, p);
-  return hipGetLastError();
+  return hipSuccess;
 }
 template <class T, int V>
 hipError_t sort_launch(const SortParams& p, SortOp op, hipStream_t stream) {

@@ -1,0 +1,92 @@
+"""Calls with more work than one launch takes (fewer than 2^32 threads): every row is done."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "mxfp8_mxfp4_experts_amd", "libmi355moe.so")
+PROBE = os.path.join(ROOT, "tests", "probe", "libnumprobe.so")
+pytestmark = pytest.mark.skipif(not (os.path.exists(LIB) and os.path.exists(PROBE)),
+                                reason="libmi355moe.so or libnumprobe.so not built")
+gpu = pytest.mark.gpu
+DEV = "cuda"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def probe():
+    lib = ctypes.CDLL(PROBE)
+    lib.probe_most_blocks.argtypes, lib.probe_most_blocks.restype = [ctypes.c_int], ctypes.c_int64
+    lib.probe_most_items.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int64]
+    lib.probe_most_items.restype = ctypes.c_int64
+    return lib
+
+
+@pytest.fixture(scope="module")
+def m():
+    import mxfp8_mxfp4_experts_amd as mod
+    return mod
+
+
+@pytest.mark.parametrize("threads", [64, 256, 512, 1024])
+def test_a_launch_stays_below_its_limit(probe, threads):
+    most = probe.probe_most_blocks(threads)
+    assert most * threads < 1 << 32 <= (most + 1) * threads
+    for per_block in (1, 4, 8):
+        for units in (1, 3, 7, 2048, 65536):
+            items = probe.probe_most_items(threads, per_block, units)
+            assert items >= 1 and -(-items * units // per_block) <= most
+            assert -(-(items + 1) * units // per_block) >= most
+
+
+@gpu
+@pytest.mark.parametrize("kind", [BF16, F32])
+def test_sort_and_unsort_of_many_short_tokens(m, kind):
+    """2^26 + 5 tokens of few elements, of which some have a row: the first, those around the
+    launches' border, the last."""
+    T, H, n = (1 << 26) + 5, 2, 16
+    at = torch.tensor([0, 3, (1 << 24) - 1, 1 << 24, (1 << 26) - 5, (1 << 26) - 4, (1 << 26) - 1,
+                       1 << 26, T - 1], device=DEV)
+    row = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    row[at] = torch.arange(len(at), dtype=torch.int32, device=DEV) + 2
+    x = torch.zeros(T, H, dtype=kind, device=DEV)
+    x[at] = torch.arange(1, 1 + len(at) * H, device=DEV).view(-1, H).to(kind)
+    rows = torch.full((n, H), 77.0, dtype=kind, device=DEV)
+    m.moe_sort_tokens(x, row, 1, rows=rows)
+    want = torch.full_like(rows, 77.0)
+    want[2:2 + len(at)] = x[at]
+    assert torch.equal(rows, want)
+    w = torch.full((T, 1), 2.0, device=DEV)
+    out = torch.full_like(x, 77.0)
+    for weights, scale in ((None, 1.0), (w, 2.0)):
+        out.fill_(77.0)
+        m.moe_unsort_tokens(rows, row, weights, 1, out=out)
+        assert torch.equal(out, x * scale)
+    drows, dw = torch.full_like(rows, 77.0), torch.full_like(w, 77.0)
+    m.moe_unsort_tokens_grad(x, rows, row, w, drows=drows, dw=dw)
+    assert torch.equal(drows[2:2 + len(at)], 2.0 * x[at]) and (drows[2 + len(at):] == 77.0).all()
+    dots = torch.zeros_like(dw)
+    dots[at, 0] = (x[at].double() ** 2).sum(1).float()   # whole numbers: exact
+    assert torch.equal(dw, dots)
+
+
+@gpu
+def test_gradients_of_many_longer_tokens(m):
+    """2^24 + 3 tokens whose rows take a workgroup each."""
+    T, H, n = (1 << 24) + 3, 520, 8
+    at = torch.tensor([0, 1 << 23, (1 << 24) - 2, (1 << 24) - 1, 1 << 24, T - 1], device=DEV)
+    row = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    row[at] = torch.arange(len(at), dtype=torch.int32, device=DEV)
+    dout = torch.empty(T, H, dtype=BF16, device=DEV)     # only the rows that have a route count
+    dout[at] = torch.randint(-4, 5, (len(at), H), device=DEV).to(BF16)
+    rows = torch.randint(-4, 5, (n, H), device=DEV).to(BF16)
+    w = torch.full((T, 1), 0.5, device=DEV)
+    drows, dw = torch.full_like(rows, 77.0), torch.full_like(w, 77.0)
+    m.moe_unsort_tokens_grad(dout, rows, row, w, drows=drows, dw=dw)
+    k = len(at)
+    assert torch.equal(drows[:k], 0.5 * dout[at]) and (drows[k:] == 77.0).all()
+    dots = torch.zeros_like(dw)
+    dots[at, 0] = (dout[at].float() * rows[:k].float()).sum(1)
+    assert torch.equal(dw, dots)
