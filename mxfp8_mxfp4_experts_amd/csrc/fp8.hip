@@ -8,6 +8,7 @@
 #include "fp8.h"
 #include "fp8_pick.h"
 #include "fp8_tile.h"
+#include "grid.h"
 #include "launch.h"
 #include "q8_dev.h"
 
@@ -326,12 +327,18 @@ __global__ __launch_bounds__(64) void fp8_far_kernel(Fp8Params p) {
 
 hipError_t launch_quant_fp8(const uint16_t* x, int64_t ld_x, int T, int H, uint8_t* xq,
                             int64_t ld_q, float* xs, int64_t ld_s, hipStream_t stream) {
-  const int per_row = (H + 511) / 512;
-  const int64_t units = (int64_t)T * per_row, blocks = (units + 4 * kQuantUnits - 1) / (4 * kQuantUnits);
-  if (units > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(quant_fp8_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x, ld_x, T, H,
-                     per_row, xq, ld_q, xs, ld_s);
-  return hipGetLastError();
+  // More tokens than a launch takes go in several (2^27 units of 512 elements in each).
+  const int per_row = (H + 511) / 512, per_block = 4 * kQuantUnits;
+  const int64_t most = most_items(256, per_block, per_row);
+  for (int64_t t = 0; t < T; t += most) {
+    const int n = (int)(T - t < most ? T - t : most);
+    const int64_t blocks = ((int64_t)n * per_row + per_block - 1) / per_block;
+    hipLaunchKernelGGL(quant_fp8_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x + t * ld_x,
+                       ld_x, n, H, per_row, xq + t * ld_q, ld_q, xs + t, ld_s);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 size_t fp8_workspace(int M, int N) { return sizeof(float) * (size_t)most_partials(M, N); }

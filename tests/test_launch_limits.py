@@ -5,6 +5,8 @@ import os
 import pytest
 import torch
 
+import fp8_ref as ref
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 LIB = os.path.join(ROOT, "mxfp8_mxfp4_experts_amd", "libmi355moe.so")
 PROBE = os.path.join(ROOT, "tests", "probe", "libnumprobe.so")
@@ -90,3 +92,25 @@ def test_gradients_of_many_longer_tokens(m):
     dots = torch.zeros_like(dw)
     dots[at, 0] = (dout[at].float() * rows[:k].float()).sum(1)
     assert torch.equal(dw, dots)
+
+
+@gpu
+def test_quantising_many_long_tokens(m):
+    """4194303 tokens of 16400 elements (137 GB): 2^27 pieces of 512 and more."""
+    T, H = (1 << 22) - 1, 16400
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 215 << 30:
+        pytest.skip("needs 215 GiB of GPU memory")
+    border = (1 << 27) // 33                       # 33 pieces a token
+    at = torch.tensor([0, border - 1, border, border + 1, T - 1], device=DEV)
+    x = torch.empty(T, H, dtype=BF16, device=DEV)  # other tokens hold anything
+    some = ref.tokens(len(at), H, 1)
+    x[at] = some.to(DEV)
+    xq = torch.empty(T, H, dtype=torch.uint8, device=DEV)
+    xq[at] = 0xAA
+    xs = torch.full((ref.blocks(H), T), -1.0, device=DEV)
+    m.moe_quant_fp8(x, xq=xq, xs=xs)
+    del x
+    q, s = ref.quant(some)
+    assert torch.equal(xq[at].cpu(), q) and torch.equal(xs[:, at].cpu(), s)
+    assert not (xs == -1.0).any()                  # a scale is positive or NaN
