@@ -248,27 +248,37 @@ template <int Q>
 int direct_steps(const Fp8Params& p) {
   return (p.K + kScaleBlock * Q * kFp8Waves - 1) / (kScaleBlock * Q * kFp8Waves);
 }
+// More tokens than a launch takes go in several.
 template <int Q>
-hipError_t direct(const Fp8Params& p, hipStream_t stream) {
+hipError_t direct(Fp8Params p, hipStream_t stream) {
   constexpr int C = 16 / Q;
-  const int64_t blocks = (int64_t)((p.M + C - 1) / C) * ((p.N + C - 1) / C);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks), block(64 * kFp8Waves);
-  const int steps = direct_steps<Q>(p);
-  if (steps == 1)
-    hipLaunchKernelGGL((fp8_direct_kernel<Q, 1>), grid, block, 0, stream, p);
-  else if (steps == 2)
-    hipLaunchKernelGGL((fp8_direct_kernel<Q, 2>), grid, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL((fp8_direct_kernel<Q, 4>), grid, block, 0, stream, p);
-  return hipGetLastError();
+  const int steps = direct_steps<Q>(p), cols = (p.N + C - 1) / C;
+  const dim3 block(64 * kFp8Waves);
+  const int64_t most = C * most_items(64 * kFp8Waves, 1, cols);
+  for (int64_t left = p.M; left > 0; left -= p.M) {
+    p.M = (int)(left < most ? left : most);
+    const dim3 grid((unsigned)((p.M + C - 1) / C * (int64_t)cols));
+    if (steps == 1)
+      hipLaunchKernelGGL((fp8_direct_kernel<Q, 1>), grid, block, 0, stream, p);
+    else if (steps == 2)
+      hipLaunchKernelGGL((fp8_direct_kernel<Q, 2>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((fp8_direct_kernel<Q, 4>), grid, block, 0, stream, p);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    p.a += p.M * p.ld_a;
+    p.sa += p.M;
+    p.out += p.M * p.ld_out;
+  }
+  return hipSuccess;
 }
 
 template <int Q, int U>
 hipError_t direct_raw(const Fp8Params& p, const uint16_t* x, int64_t ld_x, hipStream_t stream) {
   constexpr int C = 16 / Q;
   const int64_t blocks = (int64_t)((p.M + C - 1) / C) * ((p.N + C - 1) / C);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  // (fp8_raw takes this kernel for a sixtieth of that at most.)
+  if (blocks > most_blocks(64 * kFp8Waves)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks), block(64 * kFp8Waves);
   const int KB = (p.K + kScaleBlock - 1) / kScaleBlock, M = p.M < C ? p.M : C;
   const size_t lds = (size_t)M * (kScaleBlock * KB + 16 + 4 * KB);

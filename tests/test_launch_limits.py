@@ -114,3 +114,25 @@ def test_quantising_many_long_tokens(m):
     q, s = ref.quant(some)
     assert torch.equal(xq[at].cpu(), q) and torch.equal(xs[:, at].cpu(), s)
     assert not (xs == -1.0).any()                  # a scale is positive or NaN
+
+
+@gpu
+def test_direct_product_of_many_tokens(m):
+    """4194303 tokens whose scales' blocks are 1 GiB apart, so that the tiled kernel does not reach
+    them; 2^22 workgroups and more. Whole numbers: exact in any order."""
+    M, N, K = (1 << 22) - 1, 272, 144
+    g = torch.Generator(device=DEV).manual_seed(1)
+    codes = lambda *n: torch.randint(-4, 5, n, generator=g, device=DEV, dtype=torch.int8  # noqa: E731
+                                     ).float().to(ref.FP8)
+    q, w, w_s = codes(M, K), codes(N, K), torch.ones(3, 2, device=DEV)
+    xs = 2.0 ** torch.randint(-1, 2, (2, M), generator=g, device=DEV).float()
+    want = m.moe_fp8_matmul(q, xs, w, w_s)
+    rows = torch.arange(0, M, 65537, device=DEV)
+    exact = (q[rows].float() * xs[:, rows].t().repeat_interleave(128, 1)[:, :K]) @ w.float().t().contiguous()
+    assert torch.equal(want[rows], exact.to(BF16))
+    step = 1 << 28
+    far = torch.empty(step + M, device=DEV).as_strided((2, M), (step, 1))
+    far.copy_(xs)
+    out = torch.full_like(want, 77.0)
+    m.moe_fp8_matmul(q, far, w, w_s, out=out)
+    assert torch.equal(out, want)
