@@ -3,6 +3,7 @@
 #pragma once
 
 #include "dense_pick.h"   // kCus, kMaxSplits, most_partials
+#include "grid.h"
 
 namespace mi355moe {
 
@@ -46,15 +47,15 @@ inline int fp8_direct_q(int M, int N, int K) {
 // at once and in fuller ones (one and two per CU; of 256 x 256 tiles half a workgroup and one), and
 // what a workgroup takes besides (first loads, epilogue); a split's join and each partial sum.
 struct Fp8Variant {
-  int bm, bn, per_cu;
+  int bm, bn, per_cu, threads;
   float one, one_fixed, two, two_fixed, join, part;
 };
 constexpr Fp8Variant kFp8Variants[] = {
-    {256, 256, 1, 1136, 5840, 1451, 10090, 0, 0},
-    {128, 128, 2, 547, 2627, 1060, 4957, 1129, 0.0029f},
-    {64, 128, 2, 338, 1936, 704, 3020, 1744, 0.0023f},
-    {64, 64, 2, 232, 1467, 463, 2103, 1993, 0.0021f},
-    {32, 64, 2, 194, 1100, 321, 1614, 2128, 0.0019f},
+    {256, 256, 1, 512, 1136, 5840, 1451, 10090, 0, 0},
+    {128, 128, 2, 256, 547, 2627, 1060, 4957, 1129, 0.0029f},
+    {64, 128, 2, 256, 338, 1936, 704, 3020, 1744, 0.0023f},
+    {64, 64, 2, 256, 232, 1467, 463, 2103, 1993, 0.0021f},
+    {32, 64, 2, 256, 194, 1100, 321, 1614, 2128, 0.0019f},
 };
 constexpr int kFp8NumVariants = sizeof(kFp8Variants) / sizeof(kFp8Variants[0]);
 
@@ -116,14 +117,22 @@ inline int fp8_raw(int M, int N, int K) {
   return best && least <= fp8_pick(M, N, K).ns + 3200.0f ? best : 0;
 }
 
+// A grouped launch: a workgroup for every tile that there can be, in eights.
+inline int64_t fp8_grouped_blocks(int bm, int bn, int R, int E, int N) {
+  const int64_t tiles = ((int64_t)R / bm + (E < R ? E : R)) * ((N + bn - 1) / bn);
+  return (tiles + 7) / 8 * 8;
+}
+
 // Grouped: the rows of each expert are known on the GPU only, so as if the R routes were spread
-// evenly over the experts, with half a tile to spare for each.
+// evenly over the experts, with half a tile to spare for each.  (Rows by the thousand million are
+// too many for a launch of small tiles.)
 inline int fp8_pick_grouped(int R, int E, int N, int K) {
   const int stages = (K + 127) / 128, used = E < R ? E : R;
   int best = 0;
   float least = 3.4e38f;
   for (int i = 0; i < kFp8NumVariants; ++i) {
     const Fp8Variant& v = kFp8Variants[i];
+    if (i > 0 && fp8_grouped_blocks(v.bm, v.bn, R, E, N) > most_blocks(v.threads)) continue;
     const int64_t tiles = (int64_t)R / v.bm + (used + 1) / 2;
     const float t = fp8_tiled_ns(v, (tiles > used ? tiles : used) * ((N + v.bn - 1) / v.bn), stages);
     if (t < least) {

@@ -30,6 +30,7 @@
 #pragma once
 
 #include "fp8.h"
+#include "fp8_pick.h"
 
 namespace mi355moe {
 
@@ -681,9 +682,10 @@ hipError_t fp8_tile_launch(const Fp8Params& p, int splits, hipStream_t stream) {
   const int KB = (p.K + kScaleBlock - 1) / kScaleBlock;
   cut.stages_per_split = (KB + splits - 1) / splits;
   cut.splits = (KB + cut.stages_per_split - 1) / cut.stages_per_split;
-  hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, MI, NI, NBUF, WPE>),
-                     dim3(cut.tiles_m * cut.tiles_n * cut.splits), dim3(64 * WM * WN), 0, stream,
-                     p, cut);
+  const int64_t grid = (int64_t)cut.tiles_m * cut.tiles_n * cut.splits;
+  if (grid > most_blocks(64 * WM * WN)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, MI, NI, NBUF, WPE>), dim3((unsigned)grid),
+                     dim3(64 * WM * WN), 0, stream, p, cut);
   if (cut.splits > 1) {
     const int64_t pieces = (int64_t)p.M * ((p.N + 3) / 4);
     hipLaunchKernelGGL(fp8_join_kernel, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0,
@@ -700,9 +702,8 @@ hipError_t fp8_grouped_launch(const Fp8Params& p, hipStream_t stream) {
   cut.tiles_m = 0;
   cut.splits = 1;
   cut.stages_per_split = (p.K + kScaleBlock - 1) / kScaleBlock;
-  const int64_t most = ((int64_t)p.M / G::BM + (p.E < p.M ? p.E : p.M)) * cut.tiles_n;
-  const int64_t grid = (most + 7) / 8 * 8;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const int64_t grid = fp8_grouped_blocks(G::BM, G::BN, p.M, p.E, p.N);
+  if (grid > most_blocks(64 * WM * WN)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((fp8_grouped_kernel<WM, WN, MI, NI, NBUF, WPE>), dim3((unsigned)grid),
                      dim3(64 * WM * WN), 0, stream, p, cut);
   return hipGetLastError();

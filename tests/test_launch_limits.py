@@ -43,6 +43,19 @@ def test_a_launch_stays_below_its_limit(probe, threads):
             assert -(-(items + 1) * units // per_block) >= most
 
 
+@pytest.mark.parametrize("R", [1, 2048, 1 << 29, (1 << 30) - 5, 1 << 30])
+def test_grouped_launches_fit(probe, R):
+    """Whatever the routes and experts, the tile taken has a workgroup for each of them (columns as
+    many as memory holds)."""
+    tiles = [(256, 256, 512), (128, 128, 256), (64, 128, 256), (64, 64, 256), (32, 64, 256)]
+    for E in (1, 2, 64, 4096):
+        for N in (1, 16, 64, 128, 129):
+            for K in (16, 128, 1024, 7168):
+                bm, bn, threads = tiles[probe.probe_fp8_grouped(R, E, N, K)]
+                blocks = (R // bm + min(E, R)) * (-(-N // bn)) + 7
+                assert blocks * threads < 1 << 32, (E, N, K)
+
+
 @gpu
 @pytest.mark.parametrize("kind", [BF16, F32])
 def test_sort_and_unsort_of_many_short_tokens(m, kind):
@@ -136,3 +149,24 @@ def test_direct_product_of_many_tokens(m):
     out = torch.full_like(want, 77.0)
     m.moe_fp8_matmul(q, far, w, w_s, out=out)
     assert torch.equal(out, want)
+
+
+@gpu
+def test_grouped_product_of_many_routes(m):
+    """2^30 routes to 16 tokens, one column: 2^24 tiles of 64 rows and more."""
+    R, E, T, k, K = 1 << 30, 3, 16, 64, 16
+    g = torch.Generator(device=DEV).manual_seed(1)
+    codes = lambda *n: torch.randint(-4, 5, n, generator=g, device=DEV, dtype=torch.int8  # noqa: E731
+                                     ).float().to(ref.FP8)
+    q, w = codes(T, K), codes(E, 1, K)
+    route = torch.arange(R, dtype=torch.int32, device=DEV) % (T * k)
+    offs = torch.tensor([0, R // 3, R - 77, R], dtype=torch.int32, device=DEV)
+    out = torch.full((R, 1), 77.0, dtype=BF16, device=DEV)
+    m.moe_fp8_grouped(q, torch.ones(1, T, device=DEV), w, torch.ones(E, 1, 1, device=DEV), offs,
+                      route, k, out=out)
+    each = (q.float() @ w[:, 0].float().t().contiguous()).to(BF16)         # [T, E], exact
+    at = offs.tolist()
+    for e in range(E):
+        for a in range(at[e], at[e + 1], 1 << 27):
+            b = min(a + (1 << 27), at[e + 1])
+            assert torch.equal(out[a:b, 0], each[(route[a:b] // k).long(), e])
