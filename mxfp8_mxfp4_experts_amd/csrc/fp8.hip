@@ -298,39 +298,52 @@ hipError_t direct_raw(const Fp8Params& p, const uint16_t* x, int64_t ld_x, hipSt
                                  : direct_raw<Q, kRawPieces>(p, x, ld_x, stream);
 }
 
-// The simple form, for tokens that 31-bit offsets do not reach: grouped, a wavefront for every 16
-// rows of an expert and 16 columns.
+// The simple form, for tokens that 31-bit offsets do not reach: grouped, a wavefront takes tiles of 16
+// rows of an expert and kFarCols columns in turn, from global loads; the bytes from the caches to the
+// CUs bound it.  (300000 tokens x 8 of 28 experts, 3584 x 7168: 528 ms; 299000 tokens, which the tiled
+// kernel reaches, 63.)
+constexpr int kFarRows = 16, kFarBlocks = 4, kFarCols = 16 * kFarBlocks;
+constexpr int kFarMost = 1 << 18;   // workgroups, which walk over the tiles
 __global__ __launch_bounds__(64) void fp8_far_kernel(Fp8Params p) {
-  const int lane = threadIdx.x, l = lane & 15, g = lane >> 4;
-  const int cols = (p.N + 15) / 16;
-  const int64_t slot = blockIdx.x / cols;
-  const int n0 = 16 * (int)(blockIdx.x - slot * cols);
+  const int lane = threadIdx.x, l = lane & 15, g = lane >> 4, per = (p.E + 63) / 64;
+  const int cols = (p.N + kFarCols - 1) / kFarCols;
   const int KB = (p.K + kScaleBlock - 1) / kScaleBlock, NB = (p.N + kScaleBlock - 1) / kScaleBlock;
-  // Slot = output row: its expert is the number of experts that end at or before it.  There is
-  // work where the row is the first of 16 of its expert.
-  int e = 0;
-  for (int i = lane; i < p.E; i += 64) e += (int64_t)p.offs[i + 1] <= slot;
-  e = __builtin_amdgcn_readlane(fp8_wave_scan(e), 63);
-  if (e >= p.E) return;
-  const int first = max(p.offs[e], 0);
-  const int64_t m1 = min(p.offs[e + 1], p.M);
-  if (slot < first || (slot - first) % 16 != 0 || m1 <= slot) return;
-  const int64_t m = slot + l < m1 ? slot + l : m1 - 1;
-  int64_t row = m;
-  if (p.route) row = min(max(p.route[m] / p.top_k, 0), p.a_rows - 1);
-  const uint8_t* ap = p.a + row * p.ld_a;
-  const uint8_t* bp = p.b + ((int64_t)e * p.N + min(n0 + l, p.N - 1)) * p.K;
-  const float* sbp = p.sb + ((int64_t)e * NB + n0 / kScaleBlock) * KB;
-  v4f acc{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb = 0; kb < KB; ++kb) {
-    const int k = kScaleBlock * kb + 16 * g;
-    const v4f t = mfma_fp8(load_piece(bp, k, p.K), load_piece(bp, k + 64, p.K),
-                           load_piece(ap, k, p.K), load_piece(ap, k + 64, p.K));
-    const float f = p.sa[kb * p.ld_sa + row] * sbp[kb];
+  const Fp8Count c = fp8_count<kFarRows>(p, per);
+  const int64_t items = (int64_t)max(__builtin_amdgcn_readlane(c.upto, 63), 0) * cols;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int slot = (int)(it / cols), n0 = (int)(it - (int64_t)slot * cols) * kFarCols;
+    const Fp8Found f = fp8_find<kFarRows>(p, per, c, slot);
+    const uint32_t in = (uint32_t)slot - (uint32_t)f.before;
+    // (As in fp8_grouped_kernel, offsets that overlap may give what is no tile of its expert.)
+    if (in >= (uint32_t)fp8_tiles_of<kFarRows>({f.first, f.end})) continue;
+    const int64_t m = f.first + (int64_t)in * kFarRows + l, own = m < f.end ? m : f.end - 1;
+    int64_t row = own;
+    if (p.route) row = min(max(p.route[own] / p.top_k, 0), p.a_rows - 1);
+    const uint8_t* ap = p.a + row * p.ld_a;
+    const uint8_t* bp[kFarBlocks];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(t[i], f, acc[i]);
+    for (int j = 0; j < kFarBlocks; ++j)
+      bp[j] = p.b + ((int64_t)f.e * p.N + min(n0 + 16 * j + l, p.N - 1)) * p.K;
+    const float* sbp = p.sb + ((int64_t)f.e * NB + n0 / kScaleBlock) * KB;
+    v4f acc[kFarBlocks];
+#pragma unroll
+    for (int j = 0; j < kFarBlocks; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int kb = 0; kb < KB; ++kb) {
+      const int k = kScaleBlock * kb + 16 * g;
+      const v4i lo = load_piece(ap, k, p.K), hi = load_piece(ap, k + 64, p.K);
+      const float s = p.sa[kb * p.ld_sa + row] * sbp[kb];
+#pragma unroll
+      for (int j = 0; j < kFarBlocks; ++j) {
+        const v4f t = mfma_fp8(load_piece(bp[j], k, p.K), load_piece(bp[j], k + 64, p.K), lo, hi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(t[i], s, acc[j][i]);
+      }
+    }
+    if (m < f.end) {
+#pragma unroll
+      for (int j = 0; j < kFarBlocks; ++j) fp8_store(p, acc[j], m, n0 + 16 * j + 4 * g);
+    }
   }
-  if (slot + l < m1) fp8_store(p, acc, slot + l, n0 + 4 * g);
 }
 
 }  // namespace
@@ -371,9 +384,10 @@ hipError_t launch_fp8(const Fp8Params& p, hipStream_t stream) {
   const bool near = (p.route ? p.a_rows : 256) * p.ld_a + p.K < limit && 4 * KB * p.ld_sa < limit;
   if (p.offs) {
     if (!near) {
-      const int64_t blocks = (int64_t)p.M * ((p.N + 15) / 16);
-      if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-      hipLaunchKernelGGL(fp8_far_kernel, dim3((unsigned)blocks), dim3(64), 0, stream, p);
+      const int64_t tiles = ((int64_t)p.M / kFarRows + (p.E < p.M ? p.E : p.M)) *
+                            ((p.N + kFarCols - 1) / kFarCols);
+      const unsigned blocks = (unsigned)(tiles < kFarMost ? tiles : kFarMost);
+      hipLaunchKernelGGL(fp8_far_kernel, dim3(blocks), dim3(64), 0, stream, p);
       return hipGetLastError();
     }
     switch (fp8_pick_grouped(p.M, p.E, p.N, p.K)) {

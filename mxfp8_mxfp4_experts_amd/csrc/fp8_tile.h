@@ -606,6 +606,52 @@ __device__ __forceinline__ int fp8_wave_scan(int v) {   // inclusive
   return v;
 }
 
+// The tiles of BM rows of all experts, expert by expert, as a wavefront counts them: its lanes each a
+// run of `per` experts.
+struct Fp8Count {
+  Fp8Span span;      // of the run's first expert
+  int own, upto;     // the run's tiles, and with those of all runs before it
+};
+template <int BM>
+__device__ __forceinline__ int fp8_tiles_of(Fp8Span s) {
+  return (s.end - s.first + BM - 1) / BM;
+}
+template <int BM>
+__device__ __forceinline__ Fp8Count fp8_count(const Fp8Params& p, int per) {
+  const int lane = threadIdx.x & 63;
+  Fp8Count c;
+  c.span = fp8_span(p, lane * per);
+  c.own = fp8_tiles_of<BM>(c.span);
+  for (int i = 1; i < per; ++i) c.own += fp8_tiles_of<BM>(fp8_span(p, lane * per + i));
+  c.upto = fp8_wave_scan(c.own);
+  return c;
+}
+// The expert of tile `slot` of these (below the last lane's `upto`), its rows and the tiles before
+// its first: the run with the tile is looked at expert by expert (up to 64 experts: one load of
+// offsets and no more).
+struct Fp8Found {
+  int e, first, end, before;
+};
+template <int BM>
+__device__ __forceinline__ Fp8Found fp8_find(const Fp8Params& p, int per, Fp8Count c, int slot) {
+  const int lane = threadIdx.x & 63;
+  Fp8Found f;
+  f.e = __ffsll((long long)__ballot(c.upto > slot)) - 1;
+  f.before = __builtin_amdgcn_readlane(c.upto - c.own, f.e);
+  int at = f.e;                      // the lane that has the expert's rows
+  if (per > 1) {
+    c.span = lane < per ? fp8_span(p, f.e * per + lane) : Fp8Span{0, 0};
+    c.own = fp8_tiles_of<BM>(c.span);
+    c.upto = f.before + fp8_wave_scan(c.own);
+    at = __ffsll((long long)__ballot(c.upto > slot)) - 1;
+    f.before = __builtin_amdgcn_readlane(c.upto - c.own, at);
+    f.e = f.e * per + at;
+  }
+  f.first = __builtin_amdgcn_readlane(c.span.first, at);
+  f.end = __builtin_amdgcn_readlane(c.span.end, at);
+  return f;
+}
+
 // Grouped: a workgroup for every tile that there can be; it counts the experts' tiles to find its
 // own, or that there is none left for it.  Each XCD takes a contiguous range of the tiles, an
 // expert's column by column, so that what runs at once on an XCD shares weights and tokens.
@@ -618,44 +664,25 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WP
 void fp8_grouped_kernel(Fp8Params p, Fp8Cut cut) {
   using G = Fp8Geom<WM, WN, MI, NI, NBUF, WPE, true>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kLds];
-  // A wavefront's lanes each count the tiles of a run of experts; then the run with this workgroup's
-  // tile is looked at expert by expert (up to 64 experts: one load of offsets and no more).
-  const int lane = threadIdx.x & 63, per = (p.E + 63) / 64;
-  auto tiles_of = [](Fp8Span s) { return (s.end - s.first + G::BM - 1) / G::BM; };
-  Fp8Span span = fp8_span(p, lane * per);
-  int own = tiles_of(span);
-  for (int i = 1; i < per; ++i) own += tiles_of(fp8_span(p, lane * per + i));
-  int upto = fp8_wave_scan(own);
+  const int per = (p.E + 63) / 64;
+  const Fp8Count c = fp8_count<G::BM>(p, per);
   // (Offsets that overlap may count more tiles than the grid has, or than 31 bits hold: what then
   // is no tile of its expert is left out below.)
   const uint32_t items = (uint32_t)min(
-      (int64_t)max(__builtin_amdgcn_readlane(upto, 63), 0) * cut.tiles_n, (int64_t)0x7FFFFFFF);
+      (int64_t)max(__builtin_amdgcn_readlane(c.upto, 63), 0) * cut.tiles_n, (int64_t)0x7FFFFFFF);
   const uint32_t x = blockIdx.x & 7, q = items >> 3, in_x = blockIdx.x >> 3;
   if (in_x >= q + (x < (items & 7))) return;
   const uint32_t it = x * q + min(x, items & 7) + in_x;
-  const int slot = (int)(it / (uint32_t)cut.tiles_n);
-  int e = __ffsll((long long)__ballot(upto > slot)) - 1;
-  int before = __builtin_amdgcn_readlane(upto - own, e);
-  int at = e;                        // the lane that has the expert's rows
-  if (per > 1) {
-    span = lane < per ? fp8_span(p, e * per + lane) : Fp8Span{0, 0};
-    own = tiles_of(span);
-    upto = before + fp8_wave_scan(own);
-    at = __ffsll((long long)__ballot(upto > slot)) - 1;
-    before = __builtin_amdgcn_readlane(upto - own, at);
-    e = e * per + at;
-  }
-  const int first = __builtin_amdgcn_readlane(span.first, at);
-  const int end = __builtin_amdgcn_readlane(span.end, at);
-  const int tiles = tiles_of({first, end});
-  const uint32_t in = it - (uint32_t)before * (uint32_t)cut.tiles_n;
+  const Fp8Found f = fp8_find<G::BM>(p, per, c, (int)(it / (uint32_t)cut.tiles_n));
+  const int tiles = fp8_tiles_of<G::BM>({f.first, f.end});
+  const uint32_t in = it - (uint32_t)f.before * (uint32_t)cut.tiles_n;
   if (in >= (uint64_t)tiles * (uint32_t)cut.tiles_n) return;
   const int tn = (int)(in / (uint32_t)tiles);
-  const int64_t m0 = first + (int64_t)((int)in - tn * tiles) * G::BM;
+  const int64_t m0 = f.first + (int64_t)((int)in - tn * tiles) * G::BM;
   fp8_tile_body<WM, WN, MI, NI, NBUF, WPE, true>(
       p, cut,
-      Fp8Tile{m0, min((int64_t)end, m0 + G::BM), tn * G::BN, 0,
-              (p.K + kScaleBlock - 1) / kScaleBlock, 0, e},
+      Fp8Tile{m0, min((int64_t)f.end, m0 + G::BM), tn * G::BN, 0,
+              (p.K + kScaleBlock - 1) / kScaleBlock, 0, f.e},
       lds);
 }
 
