@@ -225,7 +225,8 @@ __device__ __forceinline__ void rank_step(int r, int r_end, int l, int nbits, in
 // launches 11.8 us, count and this 6.9, this alone 5.3; 16384 over 28: 7.2 and 7.5; 32768 over 28:
 // 15.8, 9.5 and 12.3; 12000 over 896: 18.2 and 12.3.)
 constexpr int kPermPlaceRoutes = 1 << 14;   // COUNT up to here: as fast, and a launch less
-constexpr int kPermPlaceCounts = 1 << 14;   // without it, the most counts that are added up anew
+constexpr int kPermPlaceCounts = 1 << 14;   // without it, the most counts that are added up anew,
+constexpr int kPermPlaceChunks = 1 << 9;    // and the most chunks whose workgroups do so
 constexpr int kPermChunkSteps = 8;   // perm_chunk_size / 64 at most
 template <bool COUNT>
 __global__ __launch_bounds__(kPermThreads) void perm_place_kernel(
@@ -341,7 +342,7 @@ hipError_t launch_permute(const int32_t* idx, int R, int offset, int E_local, in
   }
   hipLaunchKernelGGL(perm_count_kernel, dim3(n_chunks), dim3(256), lds, stream, idx, R, offset,
                      E_local, chunk, counts);
-  if ((int64_t)n_chunks * E_local <= kPermPlaceCounts) {
+  if (n_chunks <= kPermPlaceChunks && (int64_t)n_chunks * E_local <= kPermPlaceCounts) {
     hipLaunchKernelGGL((perm_place_kernel<false>), place_grid, place_block, 2 * lds, stream, idx, R,
                        offset, E_local, chunk, n_chunks, counts, offs, sorted_route, route_row,
                        tile_prefix);
