@@ -111,6 +111,7 @@ __global__ __launch_bounds__(64 * kColWaves) void perm_colscan_kernel(
 
 // Expert totals -> expert offsets, tile prefixes and the tile -> expert map;
 // grouped rows past the kept count get -1.
+constexpr int kLaneTiles = 64;   // map entries of an expert that one lane writes (25 ns each)
 __device__ __forceinline__ void perm_scan_block(int R, int E_local, const int32_t* totals,
                                                 int32_t* __restrict__ expert_offsets,
                                                 int32_t* __restrict__ sorted_route,
@@ -163,18 +164,27 @@ __device__ __forceinline__ void perm_scan_block(int R, int E_local, const int32_
   // Then each expert's offset, its tile prefixes and its entries of the
   // tile -> expert map.
   int32_t* const tile_map = tile_prefix + kNumTileSizes * (E_local + 1);
-  for (int e = e0; e < e0 + per && e < E_local; ++e) {
-    expert_offsets[e] = excl[0];
-    const int total = totals[e];
+  for (int j = 0; j < per; ++j) {
+    const int e = e0 + j;
+    const bool ok = e < E_local;
+    const int total = ok ? totals[e] : 0;
+    if (ok) {
+      expert_offsets[e] = excl[0];
+#pragma unroll
+      for (int i = 0; i < kNumTileSizes; ++i) tile_prefix[i * (E_local + 1) + e] = excl[1 + i];
+    }
+    // An expert of many tiles is written by its wavefront's lanes together.
+    const int n = tiles_of(total, kMapTileIndex), first = excl[1 + kMapTileIndex];
+    if (n <= kLaneTiles)
+      for (int t = 0; t < n; ++t) tile_map[first + t] = e;
+    for (uint64_t many = __ballot(n > kLaneTiles); many; many &= many - 1) {
+      const int l = __ffsll((long long)many) - 1;
+      const int at = __shfl(first, l), end = at + __shfl(n, l), of = __shfl(e, l);
+      for (int t = at + lane; t < end; t += 64) tile_map[t] = of;
+    }
     excl[0] += total;
 #pragma unroll
-    for (int i = 0; i < kNumTileSizes; ++i) {
-      tile_prefix[i * (E_local + 1) + e] = excl[1 + i];
-      const int n = tiles_of(total, i);
-      if (i == kMapTileIndex)
-        for (int t = 0; t < n; ++t) tile_map[excl[1 + i] + t] = e;
-      excl[1 + i] += n;
-    }
+    for (int i = 0; i < kNumTileSizes; ++i) excl[1 + i] += tiles_of(total, i);
   }
   const int n_kept = n_kept_s;
   for (int r = n_kept + tid; r < R; r += kPermThreads) sorted_route[r] = -1;
@@ -221,9 +231,11 @@ __device__ __forceinline__ void rank_step(int r, int r_end, int l, int nbits, in
 
 // Column scan, scan of the totals and ranking as one launch: every chunk's workgroup adds up the
 // counts of the chunks before its own itself, and one more workgroup writes the schedule.  COUNT:
-// and counts all routes itself, without the count kernel.  (3000 routes over 32 experts: four
-// launches 11.8 us, count and this 6.9, this alone 5.3; 16384 over 28: 7.2 and 7.5; 32768 over 28:
-// 15.8, 9.5 and 12.3; 12000 over 896: 18.2 and 12.3.)
+// and counts all routes itself, without the count kernel.  (3000 routes over 32 experts: four launches
+// 11.7 us, count and this 7.1, this alone 5.3, all to one expert 7.2 and 7.3; 16384 over 28: 7.4 and
+// 7.5, to one 7.4 and 18.6; 32768 over 28: four launches 16.0, 9.5 and 12.1; 12000 over 896: 18.4 and
+// 12.3.  Every workgroup adds up all chunks: 262144 over 8 18.2 us and 22.3 in four launches, 524288
+// 37.6 and 32.4.)
 constexpr int kPermPlaceRoutes = 1 << 14;   // COUNT up to here: as fast, and a launch less
 constexpr int kPermPlaceCounts = 1 << 14;   // without it, the most counts that are added up anew,
 constexpr int kPermPlaceChunks = 1 << 9;    // and the most chunks whose workgroups do so
@@ -235,8 +247,8 @@ __global__ __launch_bounds__(kPermThreads) void perm_place_kernel(
     int32_t* __restrict__ sorted_route, int32_t* __restrict__ route_row,
     int32_t* __restrict__ tile_prefix) {
   extern __shared__ int place_s[];
-  int* const total_s = place_s;
-  int* const before_s = place_s + E_local;
+  int* const before_s = place_s;             // of the chunks before this one
+  int* const after_s = place_s + E_local;    // of this one and those after it
   const int own = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r0 = own * chunk, r_end = min(r0 + chunk, R);
   int l[kPermChunkSteps];
@@ -248,43 +260,42 @@ __global__ __launch_bounds__(kPermThreads) void perm_place_kernel(
   for (int e = tid; e < 2 * E_local; e += kPermThreads) place_s[e] = 0;
   __syncthreads();
   if constexpr (COUNT) {
+    // One addition a route: many to one place take their turns.
 #pragma unroll 4
     for (int r = tid; r < R; r += kPermThreads) {
       const int e = local_expert(idx, r, R, offset, E_local);
-      if (e >= 0) {
-        atomicAdd(&total_s[e], 1);
-        if (r < r0) atomicAdd(&before_s[e], 1);
-      }
+      if (e >= 0) atomicAdd(r < r0 ? &before_s[e] : &after_s[e], 1);
     }
   } else {
     for (int e = lane; e < E_local; e += 64) {
-      int total = 0, before = 0;
+      int before = 0, after = 0;
 #pragma unroll 4
       for (int c = wave; c < n_chunks; c += kPermWaves) {
         const int v = counts[(size_t)c * E_local + e];
-        total += v;
         before += c < own ? v : 0;
+        after += c < own ? 0 : v;
       }
-      if (total) atomicAdd(&total_s[e], total);
       if (before) atomicAdd(&before_s[e], before);
+      if (after) atomicAdd(&after_s[e], after);
     }
   }
   __syncthreads();
   if (own == n_chunks) {
-    perm_scan_block(R, E_local, total_s, expert_offsets, sorted_route, tile_prefix);
+    perm_scan_block(R, E_local, before_s, expert_offsets, sorted_route, tile_prefix);
     return;
   }
   if (wave != 0) return;
   int run = 0;
   for (int e0 = 0; e0 < E_local; e0 += 64) {
-    const int e = e0 + lane, own_total = e < E_local ? total_s[e] : 0;
+    const int e = e0 + lane, own_before = e < E_local ? before_s[e] : 0;
+    const int own_total = e < E_local ? own_before + after_s[e] : 0;
     int x = own_total;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int y = __shfl_up(x, off);
       if (lane >= off) x += y;
     }
-    if (e < E_local) before_s[e] += run + x - own_total;
+    if (e < E_local) before_s[e] = own_before + run + x - own_total;
     run += __shfl(x, 63);
   }
   int nbits = 0;
