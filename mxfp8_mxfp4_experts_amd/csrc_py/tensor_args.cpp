@@ -178,11 +178,16 @@ class Args {
   int64_t idx_;
 };
 
-template <class F>
-F* function(PyObject* address) {
-  void* p = PyLong_AsVoidPtr(address);
-  need(p != nullptr);
-  return reinterpret_cast<F*>(p);
+// The C call, during which other Python threads run (it may load code or wait for a full queue).
+template <class F, class... A>
+moe_status_t call(PyObject* address, A... args) {
+  F* const f = reinterpret_cast<F*>(PyLong_AsVoidPtr(address));
+  need(f != nullptr);
+  moe_status_t status;
+  Py_BEGIN_ALLOW_THREADS
+  status = f(args...);
+  Py_END_ALLOW_THREADS
+  return status;
 }
 int whole_number(PyObject* o) {
   const long v = PyLong_Check(o) ? PyLong_AsLong(o) : -1;
@@ -222,9 +227,9 @@ PyObject* quant_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto q = g.codes(a[3], x.rows, x.cols);
     need(q.ld == x.cols);
     const auto s = g.rows(a[4], (x.cols + 127LL) / 128, x.rows, kF32);
-    return function<decltype(moe_quant_fp8)>(a[0])(as<uint16_t>(x.p), x.ld, x.rows, x.cols,
-                                                   as<uint8_t>(q.p), as<float>(s.p), s.ld,
-                                                   g.stream(a[1]));
+    return call<decltype(moe_quant_fp8)>(
+        a[0], as<uint16_t>(x.p), x.ld, x.rows, x.cols, as<uint8_t>(q.p), as<float>(s.p), s.ld,
+        g.stream(a[1]));
   });
 }
 
@@ -238,8 +243,8 @@ PyObject* fp8_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto o = g.rows(a[6], q.rows, w.N, kBf16);
     int bytes;
     void* ws = g.flat(a[7], ScalarType::Byte, -1, &bytes);
-    return function<decltype(moe_fp8_matmul)>(a[0])(
-        as<uint8_t>(q.p), q.ld, as<float>(s.p), s.ld, w.w, w.s, q.rows, w.N, q.cols,
+    return call<decltype(moe_fp8_matmul)>(
+        a[0], as<uint8_t>(q.p), q.ld, as<float>(s.p), s.ld, w.w, w.s, q.rows, w.N, q.cols,
         as<uint16_t>(o.p), o.ld, ws, (size_t)bytes, g.stream(a[1]));
   });
 }
@@ -253,9 +258,9 @@ PyObject* fp8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto o = g.rows(a[5], x.rows, w.N, kBf16);
     int bytes;
     void* ws = g.flat(a[6], ScalarType::Byte, -1, &bytes);
-    return function<decltype(moe_fp8_linear)>(a[0])(as<uint16_t>(x.p), x.ld, w.w, w.s, x.rows, w.N,
-                                                    x.cols, as<uint16_t>(o.p), o.ld, ws,
-                                                    (size_t)bytes, g.stream(a[1]));
+    return call<decltype(moe_fp8_linear)>(
+        a[0], as<uint16_t>(x.p), x.ld, w.w, w.s, x.rows, w.N, x.cols, as<uint16_t>(o.p), o.ld, ws,
+        (size_t)bytes, g.stream(a[1]));
   });
 }
 
@@ -270,8 +275,8 @@ PyObject* fp8_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int R = q.rows;
     void* route = a[7] == Py_None ? nullptr : g.flat(a[7], kI32, -1, &R);
     const auto o = g.rows(a[9], R, w.N, kBf16);
-    return function<decltype(moe_fp8_grouped)>(a[0])(
-        as<uint8_t>(q.p), q.ld, as<float>(s.p), s.ld, q.rows, w.w, w.s, w.E, w.N, q.cols,
+    return call<decltype(moe_fp8_grouped)>(
+        a[0], as<uint8_t>(q.p), q.ld, as<float>(s.p), s.ld, q.rows, w.w, w.s, w.E, w.N, q.cols,
         as<int32_t>(offs), as<int32_t>(route), whole_number(a[8]), R, as<uint16_t>(o.p), o.ld,
         g.stream(a[1]));
   });
@@ -285,9 +290,9 @@ PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int k = whole_number(a[4]);
     const int32_t* route = g.routes(a[3], x.rows, k);
     const auto r = g.rows(a[5], -1, x.cols, x.type);
-    return function<decltype(moe_sort_tokens)>(a[0])(x.p, x.ld, x.rows, x.cols, k, route,
-                                                     row_type(x.type), r.p, r.ld, r.rows,
-                                                     g.stream(a[1]));
+    return call<decltype(moe_sort_tokens)>(
+        a[0], x.p, x.ld, x.rows, x.cols, k, route, row_type(x.type), r.p, r.ld, r.rows,
+        g.stream(a[1]));
   });
 }
 
@@ -301,9 +306,9 @@ PyObject* unsort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* route = g.routes(a[3], -1, k, &T);
     void* w = a[4] == Py_None ? nullptr : g.whole(a[4], kF32, T, k);
     const auto o = g.rows(a[6], T, r.cols, r.type);
-    return function<decltype(moe_unsort_tokens)>(a[0])(r.p, r.ld, r.rows, T, r.cols, k, route,
-                                                       as<float>(w), row_type(r.type), o.p, o.ld,
-                                                       g.stream(a[1]));
+    return call<decltype(moe_unsort_tokens)>(
+        a[0], r.p, r.ld, r.rows, T, r.cols, k, route, as<float>(w), row_type(r.type), o.p, o.ld,
+        g.stream(a[1]));
   });
 }
 
@@ -320,9 +325,9 @@ PyObject* unsort_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* route = g.routes(a[4], d.rows, k);
     const auto o = g.rows(a[6], r.rows, d.cols, d.type);
     void* dw = g.whole(a[7], kF32, d.rows, k);
-    return function<decltype(moe_unsort_tokens_grad)>(a[0])(
-        d.p, d.ld, r.p, r.ld, r.rows, d.rows, d.cols, k, route, as<float>(w), row_type(d.type), o.p,
-        o.ld, as<float>(dw), g.stream(a[1]));
+    return call<decltype(moe_unsort_tokens_grad)>(
+        a[0], d.p, d.ld, r.p, r.ld, r.rows, d.rows, d.cols, k, route, as<float>(w),
+        row_type(d.type), o.p, o.ld, as<float>(dw), g.stream(a[1]));
   });
 }
 
@@ -341,10 +346,9 @@ PyObject* permute(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* offs = g.flat(a[6], kI32, E + 1LL);
     void* sorted = g.flat(a[7], kI32, T * k);
     void* row = g.flat(a[8], kI32, T * k);
-    return function<decltype(moe_permute)>(a[0])(as<int32_t>(ids), (int)T, (int)k, first, E,
-                                                 as<int32_t>(offs), as<int32_t>(sorted),
-                                                 as<int32_t>(row), ws, (size_t)bytes,
-                                                 g.stream(a[1]));
+    return call<decltype(moe_permute)>(
+        a[0], as<int32_t>(ids), (int)T, (int)k, first, E, as<int32_t>(offs), as<int32_t>(sorted),
+        as<int32_t>(row), ws, (size_t)bytes, g.stream(a[1]));
   });
 }
 
