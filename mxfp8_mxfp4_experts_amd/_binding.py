@@ -531,7 +531,14 @@ class _Calls:
     of a call whose buffers are all given and plainly right, else None."""
 
     def __getattr__(self, name):
-        _load_args()
+        try:
+            _load_args()
+        except ImportError:
+            # The grouping's own checks need no helper; the other calls say that it is missing.
+            if name != "permute":
+                raise
+            self.permute = lambda *args: None
+            return self.permute
         from . import _tensor_args
         setattr(self, name, getattr(_tensor_args, name))
         return getattr(self, name)
