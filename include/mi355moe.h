@@ -521,7 +521,9 @@ moe_status_t moe_quant_fp8(const uint16_t* x, int64_t ld_x, int T, int H, uint8_
 size_t moe_fp8_workspace_size(int M, int N, int K);
 
 /* Bytes of workspace for moe_fp8_matmul alone: the partial sums, at most
- * 16 MB.  It grows with M.  0 where none is needed and for invalid sizes. */
+ * 16 MB.  It grows with M (so products of many rows, which are not split, name
+ * it as well).  0 for up to 8 rows and for K up to 640, which are never split,
+ * and for invalid sizes; workspace may be NULL then. */
 size_t moe_fp8_matmul_workspace_size(int M, int N, int K);
 
 moe_status_t moe_fp8_matmul(const uint8_t* xq, int64_t ld_xq, const float* xs, int64_t ld_xs,

@@ -940,7 +940,7 @@ def moe_fp8_workspace_size(M: int, N: int, K: int) -> int:
 
 def moe_fp8_matmul_workspace_size(M: int, N: int, K: int) -> int:
     """Workspace bytes of moe_fp8_matmul alone; a buffer for M rows serves
-    fewer."""
+    fewer.  0 for up to 8 rows and for K up to 640."""
     return lib().moe_fp8_matmul_workspace_size(M, N, K)
 
 

@@ -83,7 +83,7 @@ struct Fp8Layout {
 Fp8Layout fp8_layout(int M, int N, int K) {
   Fp8Layout l;
   const int64_t blocks = ((int64_t)K + 127) / 128;
-  l.xq = align256(fp8_workspace(M, N));
+  l.xq = align256(fp8_workspace(M, N, K));
   l.ld_q = blocks * 128;
   l.ld_s = ((int64_t)M + 3) / 4 * 4;
   l.xs = align256(l.xq + (size_t)M * l.ld_q);

@@ -364,7 +364,9 @@ hipError_t launch_quant_fp8(const uint16_t* x, int64_t ld_x, int T, int H, uint8
   return hipSuccess;
 }
 
-size_t fp8_workspace(int M, int N) { return sizeof(float) * (size_t)most_partials(M, N); }
+size_t fp8_workspace(int M, int N, int K) {
+  return fp8_may_split(M, K) ? sizeof(float) * (size_t)most_partials(M, N) : 0;
+}
 
 int fp8_raw_q(int M, int N, int K) { return fp8_raw(M, N, K); }
 

@@ -72,6 +72,13 @@ struct Fp8Pick {
   float ns;      // estimated
 };
 
+// Splits are for launches that leave CUs idle; each has three stages at least.
+inline int fp8_most_splits(int K) {
+  const int stages = (K + 127) / 128;
+  return kMaxSplits < stages / 3 ? kMaxSplits : stages / 3;
+}
+inline bool fp8_may_split(int M, int K) { return M > kFp8DirectRows && fp8_most_splits(K) > 1; }
+
 inline Fp8Pick fp8_pick(int M, int N, int K) {
   Fp8Pick best{-1, 1, 3.4e38f};
   if (M <= kFp8DirectMost) {
@@ -81,8 +88,7 @@ inline Fp8Pick fp8_pick(int M, int N, int K) {
   if (M <= kFp8DirectRows) return best;
   const int stages = (K + 127) / 128;
   const int64_t sums = (int64_t)M * ((N + 3) / 4 * 4);
-  // Splits are for launches that leave CUs idle; each has three stages at least.
-  int most = kMaxSplits < stages / 3 ? kMaxSplits : stages / 3;
+  int most = fp8_most_splits(K);
   while (most > 1 && most * sums > most_partials(M, N)) --most;
   for (int i = 0; i < kFp8NumVariants; ++i) {
     const Fp8Variant& v = kFp8Variants[i];

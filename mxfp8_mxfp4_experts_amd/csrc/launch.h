@@ -146,7 +146,7 @@ struct Fp8Params {
   int top_k;
   int a_rows;
 };
-size_t fp8_workspace(int M, int N);   // grows with M
+size_t fp8_workspace(int M, int N, int K);   // grows with M
 hipError_t launch_quant_fp8(const uint16_t* x, int64_t ld_x, int T, int H, uint8_t* xq,
                             int64_t ld_q, float* xs, int64_t ld_s, hipStream_t stream);
 hipError_t launch_fp8(const Fp8Params& p, hipStream_t stream);
