@@ -393,21 +393,21 @@ hipError_t launch_fp8(const Fp8Params& p, hipStream_t stream) {
       return hipGetLastError();
     }
     switch (fp8_pick_grouped(p.M, p.E, p.N, p.K)) {
-      case 0: return fp8_grouped_launch<4, 2, 4, 8, 2, 2>(p, stream);
-      case 1: return fp8_grouped_launch<2, 2, 4, 4, 2, 2>(p, stream);
-      case 2: return fp8_grouped_launch<2, 2, 2, 4, 3, 2>(p, stream);
-      case 3: return fp8_grouped_launch<2, 2, 2, 2, 4, 2>(p, stream);
-      default: return fp8_grouped_launch<2, 2, 1, 2, 4, 2>(p, stream);
+      case 0: return fp8_grouped_launch<4, 2, 4, 8, 2>(p, stream);
+      case 1: return fp8_grouped_launch<2, 2, 4, 4, 2>(p, stream);
+      case 2: return fp8_grouped_launch<2, 2, 2, 4, 3>(p, stream);
+      case 3: return fp8_grouped_launch<2, 2, 2, 2, 4>(p, stream);
+      default: return fp8_grouped_launch<2, 2, 1, 2, 4>(p, stream);
     }
   }
   const Fp8Pick k = fp8_pick(p.M, p.N, p.K);
   if (k.variant >= 0 && near) {
     switch (k.variant) {
-      case 0: return fp8_tile_launch<4, 2, 4, 8, 2, 2>(p, k.splits, stream);
-      case 1: return fp8_tile_launch<2, 2, 4, 4, 2, 2>(p, k.splits, stream);
-      case 2: return fp8_tile_launch<2, 2, 2, 4, 3, 2>(p, k.splits, stream);
-      case 3: return fp8_tile_launch<2, 2, 2, 2, 4, 2>(p, k.splits, stream);
-      default: return fp8_tile_launch<2, 2, 1, 2, 4, 2>(p, k.splits, stream);
+      case 0: return fp8_tile_launch<4, 2, 4, 8, 2>(p, k.splits, stream);
+      case 1: return fp8_tile_launch<2, 2, 4, 4, 2>(p, k.splits, stream);
+      case 2: return fp8_tile_launch<2, 2, 2, 4, 3>(p, k.splits, stream);
+      case 3: return fp8_tile_launch<2, 2, 2, 2, 4>(p, k.splits, stream);
+      default: return fp8_tile_launch<2, 2, 1, 2, 4>(p, k.splits, stream);
     }
   }
   switch (fp8_direct_q(p.M, p.N, p.K)) {

@@ -51,14 +51,15 @@ struct Fp8Tile {
   int n0, s0, s1, split, expert;
 };
 
-template <int WM, int WN, int MI, int NI, int NBUF, int WPE, bool GROUPED>
+template <int WM, int WN, int MI, int NI, int NBUF>
 struct Fp8Geom {
   static constexpr int W = WM * WN, BM = 16 * MI * WM, BN = 16 * NI * WN;
-  // 1 KB loads (8 rows) per wavefront and stage; where they do not share out evenly the last ones
-  // are done twice.
-  static constexpr int PA = (BM / 8 + W - 1) / W, PB = (BN / 8 + W - 1) / W;
+  // 1 KB loads (8 rows) per wavefront and stage.
+  static constexpr int PA = BM / 8 / W, PB = BN / 8 / W;
+  static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0, "loads share out evenly");
   // The tokens' scales come for kGroup stages at a time, 64 of them a load (a load per wavefront
-  // in every stage took 11% of a 64 x 64 product's time).
+  // in every stage took 11% of a 64 x 64 product's time); where the loads do not share out evenly the
+  // last ones are done twice.
   static constexpr int kGroup = 4, kTokS = kGroup * BM / 64, PS = (kTokS + W - 1) / W;
   // Rings: NBUF stages of tokens, NBUF of weights, 3 groups of scales.
   static constexpr int kStageA = BM * 128, kStageB = BN * 128;
@@ -66,16 +67,16 @@ struct Fp8Geom {
   static constexpr int kScales = 3 * kGroup;
   static constexpr int kLds = kOffS + kScales * BM * 4;
   // Room for two stages' operands in registers.
-  static constexpr bool kFull = 16 * (MI + NI) + 4 * MI * NI <= (WPE == 4 ? 64 : 144);
+  static constexpr bool kFull = 16 * (MI + NI) + 4 * MI * NI <= 144;
 };
 
-template <int WM, int WN, int MI, int NI, int NBUF, int WPE, bool GROUPED>
+template <int WM, int WN, int MI, int NI, int NBUF, bool GROUPED>
 __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& cut,
                                               const Fp8Tile& t, uint8_t* lds) {
-  using G = Fp8Geom<WM, WN, MI, NI, NBUF, WPE, GROUPED>;
+  using G = Fp8Geom<WM, WN, MI, NI, NBUF>;
   constexpr int BM = G::BM, BN = G::BN, PA = G::PA, PB = G::PB, PS = G::PS;
   static_assert((NBUF - 1) * (PA + PB) < 64, "vmcnt");
-  constexpr int NX = 128 % (16 * NI) == 0 ? 1 : 2;   // weight scale blocks that a wavefront meets
+  static_assert(kScaleBlock % (16 * NI) == 0, "a wavefront's columns share their scales");
   fp8_lds_t* const lds_base = (fp8_lds_t*)lds;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -111,13 +112,13 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
   uint32_t va[PA], vb[PB], vs[PS];
 #pragma unroll
   for (int q = 0; q < PA; ++q) {
-    const int row = 8 * min(PA * wave + q, BM / 8 - 1) + lrow;
+    const int row = 8 * (PA * wave + q) + lrow;
     const int64_t at = gather ? (int64_t)token(row) : row;
     va[q] = row < rows_a ? (uint32_t)(at * p.ld_a) + 16 * chunk : kFp8PastEnd;
   }
 #pragma unroll
   for (int q = 0; q < PB; ++q) {
-    const int row = 8 * min(PB * wave + q, BN / 8 - 1) + lrow;
+    const int row = 8 * (PB * wave + q) + lrow;
     vb[q] = row < rows_b ? (uint32_t)(row * p.K) + 16 * chunk : kFp8PastEnd;
   }
 #pragma unroll
@@ -151,25 +152,22 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
   };
   auto issue_a = [&](int q, int s, int buf) __attribute__((always_inline)) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        ra, lds + buf * G::kStageA + 1024 * min(PA * wave + q, BM / 8 - 1), 16, va[q],
+        ra, lds + buf * G::kStageA + 1024 * (PA * wave + q), 16, va[q],
         kScaleBlock * min(s, KB - 1), 0, 0);
   };
   auto issue_b = [&](int q, int s, int buf) __attribute__((always_inline)) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rb, lds + G::kOffB + buf * G::kStageB + 1024 * min(PB * wave + q, BN / 8 - 1), 16, vb[q],
+        rb, lds + G::kOffB + buf * G::kStageB + 1024 * (PB * wave + q), 16, vb[q],
         kScaleBlock * min(s, KB - 1), 0, 0);
   };
 
   // The weight's scales: lane l has those of stage (s0 + 64 n) + l.
   const int n_wave = t.n0 + 16 * NI * wn;
   const int n_blocks = (p.N + kScaleBlock - 1) / kScaleBlock;
-  float vsb[NX];
+  float vsb;
   auto load_sb = [&](int s) __attribute__((always_inline)) {
-#pragma unroll
-    for (int x = 0; x < NX; ++x)
-      vsb[x] = p.sb[((int64_t)t.expert * n_blocks +
-                     min(n_wave / kScaleBlock + x, n_blocks - 1)) * KB +
-                    min(s + lane, KB - 1)];
+    vsb = p.sb[((int64_t)t.expert * n_blocks + min(n_wave / kScaleBlock, n_blocks - 1)) * KB +
+               min(s + lane, KB - 1)];
   };
   load_sb(t.s0);
 
@@ -266,10 +264,7 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
       read_s(C, o.s);
     };
     auto step = [&](int s, int at, const Set& o, Set& next) __attribute__((always_inline)) {
-      float sb[NX];
-#pragma unroll
-      for (int x = 0; x < NX; ++x)
-        sb[x] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vsb[x]), at));
+      const float sb = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vsb), at));
       const int nbuf = buf + 1 == NBUF ? 0 : buf + 1;
       cut_off(s + NBUF);
       __builtin_amdgcn_sched_barrier(0);
@@ -284,13 +279,10 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
       for (int q = 0; q < PB; ++q) issue_b(q, s + NBUF, buf);
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
-        float sj = sb[0];
-        if constexpr (NX == 2)
-          sj = (n_wave + 16 * j) / kScaleBlock == n_wave / kScaleBlock ? sb[0] : sb[1];
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
           add(i, (j + NI - 1) % NI);
-          if (NX == 2 || j == 0) f[i] = o.s[i] * sj;
+          if (j == 0) f[i] = o.s[i] * sb;
           prod[i] = mfma_fp8(o.b[j].lo, o.b[j].hi, o.a[i].lo, o.a[i].hi);
         }
       }
@@ -308,8 +300,7 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
     // 64 stages at a time: see below.
     for (int c0 = t.s0; c0 < t.s1; c0 += 64) {
       if (c0 > t.s0) load_sb(c0);
-#pragma unroll
-      for (int x = 0; x < NX; ++x) asm volatile("" : "+v"(vsb[x]));
+      asm volatile("" : "+v"(vsb));
       const int n = min(t.s1 - c0, 64);
 #pragma unroll 1
       for (int at = 0; at + 1 < n; at += 2) {
@@ -320,8 +311,9 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
     }
   } else {
     // Weight operands in registers: the current column's and the next two, in a ring that comes out
-    // even with the columns where that costs no more registers.
-    constexpr int F = NI % 4 == 0 ? 4 : 3;
+    // even with the columns.
+    constexpr int F = 4;
+    static_assert(NI % F == 0, "a stage's first column is in the ring's first place");
     Op fa[MI], fb[F];
     float fs[MI];                     // the tokens' scales
     {
@@ -336,7 +328,7 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
     // operands are in registers from the stage's start, so where there are columns enough a barrier
     // of their own, JA, frees the tokens' buffer almost a stage earlier: their loads and the
     // weights' then take turns, and each has about a stage's time to come.
-    constexpr int JB = NI > 2 ? NI - 2 : NI - 1;
+    constexpr int JB = NI - 2;
     constexpr int JA = NI == 8 ? 1 : JB;
     constexpr int kBehind = JA < JB ? PA : 0;   // loads behind those that JB waits for
     if (16 * MI * wm >= rows_a) {
@@ -371,21 +363,17 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
     // would wait for all loads in every stage before it reads a lane of it.
     for (int c0 = t.s0; c0 < t.s1; c0 += 64) {
       if (c0 > t.s0) load_sb(c0);
-#pragma unroll
-      for (int x = 0; x < NX; ++x) asm volatile("" : "+v"(vsb[x]));
+      asm volatile("" : "+v"(vsb));
       const int c1 = min(t.s1, c0 + 64);
 #pragma unroll 1
       for (int s = c0; s < c1; ++s) {
-        float sb[NX];
-#pragma unroll
-        for (int x = 0; x < NX; ++x)
-          sb[x] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vsb[x]), s - c0));
+        const float sb = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vsb), s - c0));
         const int next = buf + 1 == NBUF ? 0 : buf + 1;
         const fp8_lds_t* B = at_lds(buf * G::kStageB);
         const fp8_lds_t* A1 = at_lds(next * G::kStageA);
         const fp8_lds_t* B1 = at_lds(next * G::kStageB);
         cut_off(s + NBUF);
-        if (NI > 1) fb[1] = read_b(B, 1);
+        fb[1] = read_b(B, 1);
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
           if (j == JA && JA < JB) {
@@ -407,7 +395,7 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
             for (int q = 0; q < (JA < JB ? JB - JA : JB) * MI; ++q) {
               __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
               __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-              __builtin_amdgcn_sched_group_barrier(0x100, MI == 1 ? 2 : 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
               __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -426,14 +414,11 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
           if (j + 2 < NI)
             fb[(j + 2) % F] = read_b(B, j + 2);
           else if (j == NI - 1)
-            fb[NI % F] = read_b(B1, 0);
-          float sj = sb[0];
-          if constexpr (NX == 2)
-            sj = (n_wave + 16 * j) / kScaleBlock == n_wave / kScaleBlock ? sb[0] : sb[1];
+            fb[0] = read_b(B1, 0);
 #pragma unroll
           for (int i = 0; i < MI; ++i) {
             add(i, (j + NI - 1) % NI);
-            if (NX == 2 || j == 0) f[i] = fs[i] * sj;
+            if (j == 0) f[i] = fs[i] * sb;
             prod[i] = mfma_fp8(fb[j % F].lo, fb[j % F].hi, fa[i].lo, fa[i].hi);
             if (j == NI - 1) fa[i] = read_a(A1, i);
           }
@@ -455,7 +440,6 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
           __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
           __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
         }
-        if constexpr (NI % F != 0) fb[0] = fb[NI % F];
         asm volatile("" ::: "memory");
         buf = next;
       }
@@ -559,10 +543,10 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Params& p, const Fp8Cut& 
   }
 }
 
-template <int WM, int WN, int MI, int NI, int NBUF, int WPE>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE)))
+template <int WM, int WN, int MI, int NI, int NBUF>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void fp8_tile_kernel(Fp8Params p, Fp8Cut cut) {
-  using G = Fp8Geom<WM, WN, MI, NI, NBUF, WPE, false>;
+  using G = Fp8Geom<WM, WN, MI, NI, NBUF>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kLds];
   // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous range, split by split, a
   // split's tiles in blocks of up to 8 tile rows walked column by column.
@@ -580,7 +564,7 @@ void fp8_tile_kernel(Fp8Params p, Fp8Cut cut) {
   const int KB = (p.K + kScaleBlock - 1) / kScaleBlock;
   const int s0 = split * cut.stages_per_split;
   const int64_t m0 = (int64_t)tm * G::BM;
-  fp8_tile_body<WM, WN, MI, NI, NBUF, WPE, false>(
+  fp8_tile_body<WM, WN, MI, NI, NBUF, false>(
       p, cut,
       Fp8Tile{m0, min((int64_t)p.M, m0 + G::BM), tn * G::BN, s0,
               min(KB, s0 + cut.stages_per_split), split, 0},
@@ -659,10 +643,10 @@ __device__ __forceinline__ Fp8Found fp8_find(const Fp8Params& p, int per, Fp8Cou
 // 316 us against 278: nothing covers a tile's first loads and its stores.  All experts' whole tiles
 // first and the last, shorter ones of each after them: in 28 experts 269 against 241, since an
 // expert's tiles then no longer share its weights.)
-template <int WM, int WN, int MI, int NI, int NBUF, int WPE>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE)))
+template <int WM, int WN, int MI, int NI, int NBUF>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void fp8_grouped_kernel(Fp8Params p, Fp8Cut cut) {
-  using G = Fp8Geom<WM, WN, MI, NI, NBUF, WPE, true>;
+  using G = Fp8Geom<WM, WN, MI, NI, NBUF>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kLds];
   const int per = (p.E + 63) / 64;
   const Fp8Count c = fp8_count<G::BM>(p, per);
@@ -679,7 +663,7 @@ void fp8_grouped_kernel(Fp8Params p, Fp8Cut cut) {
   if (in >= (uint64_t)tiles * (uint32_t)cut.tiles_n) return;
   const int tn = (int)(in / (uint32_t)tiles);
   const int64_t m0 = f.first + (int64_t)((int)in - tn * tiles) * G::BM;
-  fp8_tile_body<WM, WN, MI, NI, NBUF, WPE, true>(
+  fp8_tile_body<WM, WN, MI, NI, NBUF, true>(
       p, cut,
       Fp8Tile{m0, min((int64_t)f.end, m0 + G::BM), tn * G::BN, 0,
               (p.K + kScaleBlock - 1) / kScaleBlock, 0, f.e},
@@ -700,9 +684,9 @@ static __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Params p, int s
   fp8_store(p, s, m, 4 * (int)(at - m * per_row));
 }
 
-template <int WM, int WN, int MI, int NI, int NBUF, int WPE>
+template <int WM, int WN, int MI, int NI, int NBUF>
 hipError_t fp8_tile_launch(const Fp8Params& p, int splits, hipStream_t stream) {
-  using G = Fp8Geom<WM, WN, MI, NI, NBUF, WPE, false>;
+  using G = Fp8Geom<WM, WN, MI, NI, NBUF>;
   Fp8Cut cut;
   cut.tiles_m = (p.M + G::BM - 1) / G::BM;
   cut.tiles_n = (p.N + G::BN - 1) / G::BN;
@@ -711,7 +695,7 @@ hipError_t fp8_tile_launch(const Fp8Params& p, int splits, hipStream_t stream) {
   cut.splits = (KB + cut.stages_per_split - 1) / cut.stages_per_split;
   const int64_t grid = (int64_t)cut.tiles_m * cut.tiles_n * cut.splits;
   if (grid > most_blocks(64 * WM * WN)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, MI, NI, NBUF, WPE>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, MI, NI, NBUF>), dim3((unsigned)grid),
                      dim3(64 * WM * WN), 0, stream, p, cut);
   if (cut.splits > 1) {
     const int64_t pieces = (int64_t)p.M * ((p.N + 3) / 4);
@@ -721,9 +705,9 @@ hipError_t fp8_tile_launch(const Fp8Params& p, int splits, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int WM, int WN, int MI, int NI, int NBUF, int WPE>
+template <int WM, int WN, int MI, int NI, int NBUF>
 hipError_t fp8_grouped_launch(const Fp8Params& p, hipStream_t stream) {
-  using G = Fp8Geom<WM, WN, MI, NI, NBUF, WPE, true>;
+  using G = Fp8Geom<WM, WN, MI, NI, NBUF>;
   Fp8Cut cut;
   cut.tiles_n = (p.N + G::BN - 1) / G::BN;
   cut.tiles_m = 0;
@@ -731,7 +715,7 @@ hipError_t fp8_grouped_launch(const Fp8Params& p, hipStream_t stream) {
   cut.stages_per_split = (p.K + kScaleBlock - 1) / kScaleBlock;
   const int64_t grid = fp8_grouped_blocks(G::BM, G::BN, p.M, p.E, p.N);
   if (grid > most_blocks(64 * WM * WN)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((fp8_grouped_kernel<WM, WN, MI, NI, NBUF, WPE>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((fp8_grouped_kernel<WM, WN, MI, NI, NBUF>), dim3((unsigned)grid),
                      dim3(64 * WM * WN), 0, stream, p, cut);
   return hipGetLastError();
 }
