@@ -545,12 +545,14 @@ moe_status_t moe_fp8_linear(const uint16_t* x, int64_t ld_x, const uint8_t* w, c
  *   gives them (read on the GPU: the call does not synchronise); out [R, N].
  *   Output rows before the first offset and behind the last are left as they
  *   were; offsets past R and routes past the tokens' rows are cut off there.
- *   Offsets do not descend: rows that descending ones give to several experts
- *   hold, element by element, one's or what was there.
- *   Tokens read through sorted_route that span 2 GiB or more ((rows - 1) * ld_xq +
- *   K), 256 rows that span as much without it, and scales that do take a simpler
- *   kernel, several times slower: many tokens are better put into expert order
- *   first (moe_sort_tokens).
+ *   Offsets do not descend.  Where they do, an expert whose end is before its
+ *   start has no rows, and the experts' rows may come to more tiles than R has:
+ *   then a row that any expert claims, one or several, holds, element by element,
+ *   a claimant's values or what was there.  Other rows are left as they were.
+ *   Tokens read through sorted_route that span 2 GiB or more (rows * ld_xq + K),
+ *   256 rows that span as much without it, and scales that do (4 * KB * ld_xs) take
+ *   a simpler kernel, several times slower: many tokens are better put into expert
+ *   order first (moe_sort_tokens).
  *   1 <= E_local <= 4096; 0 <= rows, R <= 2^30; without sorted_route rows >= R. */
 moe_status_t moe_fp8_grouped(const uint8_t* xq, int64_t ld_xq, const float* xs, int64_t ld_xs,
                              int rows, const uint8_t* w, const float* w_s, int E_local, int N,
