@@ -10,6 +10,7 @@
 // bytes (by the hardware scaled conversion where the group is finite); the
 // first lane of the group writes the scale byte.
 #include "common.h"
+#include "grid.h"
 #include "launch.h"
 #include "quant_dev.h"
 
@@ -31,9 +32,16 @@ __global__ __launch_bounds__(256) void quant_kernel(const uint16_t* __restrict__
 
 hipError_t launch_quant(const uint16_t* x, int64_t ld, int T, int H, uint8_t* xq, uint8_t* xs,
                         hipStream_t stream) {
-  if (T <= 0) return hipSuccess;
-  hipLaunchKernelGGL(quant_kernel, dim3(T), dim3(256), 0, stream, x, ld, H, xq, xs);
-  return hipGetLastError();
+  // More tokens than a launch takes (2^24) go in several.
+  const int64_t most = most_blocks(256);
+  for (int64_t t = 0; t < T; t += most) {
+    const unsigned n = (unsigned)(T - t < most ? T - t : most);
+    hipLaunchKernelGGL(quant_kernel, dim3(n), dim3(256), 0, stream, x + t * ld, ld, H, xq + t * H,
+                       xs + t * (H / 32));
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace mi355moe

@@ -170,3 +170,18 @@ def test_grouped_product_of_many_routes(m):
         for a in range(at[e], at[e + 1], 1 << 27):
             b = min(a + (1 << 27), at[e + 1])
             assert torch.equal(out[a:b, 0], each[(route[a:b] // k).long(), e])
+
+
+@gpu
+def test_mxfp8_quantisation_of_many_tokens(m):
+    """2^24 + 3 tokens, a workgroup each."""
+    T, H = (1 << 24) + 3, 32
+    at = torch.tensor([0, 1, (1 << 24) - 2, (1 << 24) - 1, 1 << 24, T - 1], device=DEV)
+    x = torch.zeros(T, H, dtype=BF16, device=DEV)
+    x[at] = ref.tokens(len(at), H, 1).to(DEV)
+    xq = torch.full((T, H), 0xAA, dtype=torch.uint8, device=DEV)
+    xs = torch.full((T, 1), 0xAA, dtype=torch.uint8, device=DEV)
+    m.moe_quant_mxfp8(x, xq=xq, xs=xs)
+    q, s = m.moe_quant_mxfp8(x[at].contiguous())
+    assert torch.equal(xq[at], q) and torch.equal(xs[at], s)
+    assert not (xs == 0xAA).any()                  # 2^43: none of these values has it
