@@ -20,6 +20,7 @@
 //    over a 64-bit key (ordered float key, then inverted expert index)
 //    restricted to keys below the previous winner.
 #include "common.h"
+#include "grid.h"
 #include "launch.h"
 #include "route_dev.h"
 
@@ -29,14 +30,14 @@ namespace {
 
 constexpr int kRouteWaves = 4;
 
-__global__ __launch_bounds__(256) void route_reg_kernel(
+__global__ __launch_bounds__(64 * kRouteWaves) void route_reg_kernel(
     const float* __restrict__ logits, int64_t ld, const float* __restrict__ bias, int T, int E,
     int K, float scaling, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
   __shared__ uint32_t keys_s[64 * kRegExpertsPerLane];
   __shared__ uint64_t cand_s[64];
   const int t = blockIdx.x;
   const float* row = logits + (size_t)t * ld;
-  for (int e = threadIdx.x; e < E; e += 256)
+  for (int e = threadIdx.x; e < E; e += 64 * kRouteWaves)
     keys_s[e] = ordered_key(sigmoid_score(row[e]) + (bias ? bias[e] : 0.0f));
   __syncthreads();
   if (threadIdx.x >= 64) return;                     // whole wavefronts leave
@@ -94,16 +95,24 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(
 
 hipError_t launch_route(const float* logits, int64_t ld, const float* bias, int T, int E, int K,
                         float scaling, int32_t* idx, float* w, hipStream_t stream) {
-  int blocks = (T + kRouteWaves - 1) / kRouteWaves;
-  if (E <= 64 * kRegExpertsPerLane) {
-    hipLaunchKernelGGL(route_reg_kernel, dim3(T), dim3(256), 0, stream, logits, ld, bias, T, E, K,
-                       scaling, idx, w);
-    return hipGetLastError();
+  // More tokens than a launch takes (2^24, or 2^26) go in several.
+  const bool reg = E <= 64 * kRegExpertsPerLane;
+  const int per_block = reg ? 1 : kRouteWaves;
+  const size_t lds = sizeof(float) * (size_t)E * kRouteWaves;
+  const int64_t most = most_items(64 * kRouteWaves, per_block, 1);
+  for (int64_t t = 0; t < T; t += most) {
+    const int n = (int)(T - t < most ? T - t : most);
+    const dim3 grid((n + per_block - 1) / per_block), block(64 * kRouteWaves);
+    if (reg)
+      hipLaunchKernelGGL(route_reg_kernel, grid, block, 0, stream, logits + t * ld, ld, bias, n, E,
+                         K, scaling, idx + t * K, w + t * K);
+    else
+      hipLaunchKernelGGL(route_kernel, grid, block, lds, stream, logits + t * ld, ld, bias, n, E, K,
+                         scaling, idx + t * K, w + t * K);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
   }
-  size_t lds = sizeof(float) * (size_t)E * kRouteWaves;
-  hipLaunchKernelGGL(route_kernel, dim3(blocks), dim3(64 * kRouteWaves), lds, stream, logits, ld,
-                     bias, T, E, K, scaling, idx, w);
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace mi355moe

@@ -185,3 +185,18 @@ def test_mxfp8_quantisation_of_many_tokens(m):
     q, s = m.moe_quant_mxfp8(x[at].contiguous())
     assert torch.equal(xq[at], q) and torch.equal(xs[at], s)
     assert not (xs == 0xAA).any()                  # 2^43: none of these values has it
+
+
+@gpu
+@pytest.mark.parametrize("T,E", [((1 << 24) + 3, 5), ((1 << 24) + 3, 1025)])
+def test_routing_of_many_tokens(m, T, E):
+    """2^24 + 3 tokens, a workgroup each up to 1024 experts."""
+    logits = torch.zeros(T, E, device=DEV)
+    at = torch.tensor([0, 1, (1 << 24) - 2, (1 << 24) - 1, 1 << 24, T - 1], device=DEV)
+    logits[at] = torch.randn(len(at), E, generator=torch.Generator().manual_seed(1)).to(DEV)
+    idx = torch.full((T, 2), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((T, 2), -7.0, device=DEV)
+    m.moe_route(logits, None, 2, topk_idx=idx, topk_w=w)
+    want, want_w = m.moe_route(logits[at].contiguous(), None, 2)
+    assert torch.equal(idx[at], want) and torch.equal(w[at], want_w)
+    assert (idx >= 0).all() and (w > 0).all()
