@@ -8,6 +8,7 @@
 // and only needs the clear and bf16 passes at the end of this file.
 #include "common.h"
 #include "fc_common.h"
+#include "grid.h"
 #include "launch.h"
 
 namespace mi355moe {
@@ -110,37 +111,48 @@ __global__ __launch_bounds__(256) void acc_to_bf16_kernel(const float* __restric
 
 }  // namespace
 
+namespace {
+
+// launch(t, n) for tokens [t, t + n): more than a launch takes, where a token is `units` lanes' or
+// workgroups' work of which a workgroup takes `per_block`, go in several.
+template <class F>
+hipError_t by_tokens(int T, int threads, int64_t per_block, int64_t units, F launch) {
+  const int64_t most = most_items(threads, per_block, units);
+  for (int64_t t = 0; t < T; t += most) {
+    const int64_t n = T - t < most ? T - t : most;
+    launch(t, n, dim3((unsigned)((n * units + per_block - 1) / per_block)));
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
 hipError_t launch_acc_clear(float* acc, int T, int H, hipStream_t stream) {
-  const int64_t n4 = (int64_t)T * H / 4;
-  if (n4 <= 0) return hipSuccess;
-  const int64_t blocks = (n4 + 255) / 256;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(acc_clear_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
-                     reinterpret_cast<float4*>(acc), n4);
-  return hipGetLastError();
+  const int64_t per_row = H / 4;
+  return by_tokens(T, 256, 256, per_row, [&](int64_t t, int64_t n, dim3 grid) {
+    hipLaunchKernelGGL(acc_clear_kernel, grid, dim3(256), 0, stream,
+                       reinterpret_cast<float4*>(acc + t * H), n * per_row);
+  });
 }
 
 hipError_t launch_acc_to_bf16(const float* acc, int T, int H, uint16_t* out, int64_t ld_out,
                               hipStream_t stream) {
-  const int64_t n8 = (int64_t)T * H / 8;
-  if (n8 <= 0) return hipSuccess;
-  const int64_t blocks = (n8 + 255) / 256;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(acc_to_bf16_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, acc, H, n8,
-                     out, ld_out);
-  return hipGetLastError();
+  const int64_t per_row = H / 8;
+  return by_tokens(T, 256, 256, per_row, [&](int64_t t, int64_t n, dim3 grid) {
+    hipLaunchKernelGGL(acc_to_bf16_kernel, grid, dim3(256), 0, stream, acc + t * H, H, n * per_row,
+                       out + t * ld_out, ld_out);
+  });
 }
 
 hipError_t launch_combine(const uint16_t* y, const int8_t* ye, int H, const int32_t* route_row,
                           const float* topk_w, int T, int K, uint16_t* out, int64_t ld_out,
                           hipStream_t stream) {
-  const int64_t blocks = (int64_t)T * ((H / 8 + 64 - 1) / 64);
-  if (blocks <= 0) return hipSuccess;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks);
-  hipLaunchKernelGGL(combine_kernel, grid, dim3(64), 0, stream, y, ye, H, route_row, topk_w, K,
-                     out, ld_out);
-  return hipGetLastError();
+  return by_tokens(T, 64, 1, (H / 8 + 64 - 1) / 64, [&](int64_t t, int64_t, dim3 grid) {
+    hipLaunchKernelGGL(combine_kernel, grid, dim3(64), 0, stream, y, ye, H, route_row + t * K,
+                       topk_w + t * K, K, out + t * ld_out, ld_out);
+  });
 }
 
 }  // namespace mi355moe

@@ -200,3 +200,44 @@ def test_routing_of_many_tokens(m, T, E):
     want, want_w = m.moe_route(logits[at].contiguous(), None, 2)
     assert torch.equal(idx[at], want) and torch.equal(w[at], want_w)
     assert (idx >= 0).all() and (w > 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("atomic", [False, True])
+def test_combine_of_many_tokens(m, atomic):
+    """2^26 + 3 tokens of 256 columns, of which some have an expert: those around the launches'
+    border and the last."""
+    T, H, I = (1 << 26) + 3, 256, 128
+    mode = m.COMBINE_ATOMIC if atomic else m.COMBINE_DETERMINISTIC
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 130 << 30:
+        pytest.skip("needs 130 GiB of GPU memory")
+    at = torch.tensor([0, 5, (1 << 26) - 2, (1 << 26) - 1, 1 << 26, T - 1], device=DEV)
+    n = len(at)
+    g = torch.Generator().manual_seed(1)
+    w2 = torch.randint(0, 256, (1, H, I // 2), generator=g, dtype=torch.uint8).to(DEV)
+    w2_s = torch.full((1, H, I // 32), 127, dtype=torch.uint8, device=DEV)
+    codes = torch.randint(0, 0x40, (n, I), generator=g, dtype=torch.uint8).to(DEV)
+
+    def run(T, at):
+        idx = torch.full((T, 1), -1, dtype=torch.int32, device=DEV)
+        idx[at] = 0
+        ws = torch.full((m.moe_workspace_size(T, 1, 1, H, I, mode),), 0x42, dtype=torch.uint8,
+                        device=DEV)
+        offs, sorted_route, row = m.moe_permute(idx, 0, 1, ws)
+        hq = torch.empty(T, I, dtype=torch.uint8, device=DEV)
+        hq[:n] = codes
+        hs = torch.empty(T, I // 32, dtype=torch.uint8, device=DEV)
+        hs[:n] = 127
+        w = torch.ones(T, 1, device=DEV)
+        out = torch.full((T, H), 77.0, dtype=BF16, device=DEV)
+        m.moe_fc2_combine(hq, hs, T, 1, offs, sorted_route, row, w, w2, w2_s, ws, out=out, mode=mode)
+        return out
+    want = run(n, torch.arange(n, device=DEV))
+    assert torch.isfinite(want).all() and (want != 0).any(1).all()
+    out = run(T, at)
+    # The two may take another kernel: one rounding of the float sum to bf16 apart (the sums differ
+    # by their order, far below that).
+    assert ((out[at].float() - want.float()).abs() <= 2.0 ** -7 * want.float().abs() + 1e-3).all()
+    out[at] = 0.0
+    assert not out.any()
