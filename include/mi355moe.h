@@ -503,6 +503,8 @@ moe_status_t moe_route_groups(const float* logits, int64_t ld_logits, const floa
  *   are NaN.
  *   With the weight transposed (w as [K, N], w_s as [KB, NB]) the same calls
  *   give the gradient with respect to the tokens: dx = dout . w.
+ *   Tokens of which 256 rows span 2 GiB (256 * ld_xq + K), and scales that do (4 *
+ *   KB * ld_xs), take the kernel of few tokens at any M, which is far slower.
  *   K a multiple of 16, 16 <= K <= 2^20; 1 <= N <= 2^20; 0 <= M <= 4194303.
  * ------------------------------------------------------------------------- */
 
@@ -510,7 +512,9 @@ moe_status_t moe_route_groups(const float* logits, int64_t ld_logits, const floa
  * nearest, ties to even, in float.  A block that holds an infinity or a NaN
  * gets the scale NaN and codes 0, so that the token's products are NaN.
  *   x  bf16 bits [T, H], row stride ld_x (>= H, multiple of 8); H as K above.
- *   xq uint8 [T, H]; xs float [ceil(H / 128), T], row stride ld_xs. */
+ *   xq uint8 [T, H]; xs float [ceil(H / 128), T], row stride ld_xs.
+ *   More tokens than a call takes are quantised in pieces: tokens [t0, t0 + T) of
+ *   a larger xs are xs + t0 with that one's ld_xs. */
 moe_status_t moe_quant_fp8(const uint16_t* x, int64_t ld_x, int T, int H, uint8_t* xq, float* xs,
                            int64_t ld_xs, hipStream_t stream);
 
@@ -565,7 +569,9 @@ moe_status_t moe_fp8_grouped(const uint8_t* xq, int64_t ld_xq, const float* xs, 
  * outside the five calls and for their training.  route_row int32 [T, top_k] as
  * moe_permute gives it; a route whose row is negative or not below n_rows has
  * no part.  Rows may have any length and stride and start at any element; sums
- * in float, in slot order, one rounding; equal calls give equal bits.
+ * in float, in slot order, one rounding; equal calls give equal bits.  (A row
+ * that several routes name, as moe_permute's never do, gets, element by element,
+ * what one of them brings.)
  * 1 <= H <= 2^20; 1 <= top_k <= 64; T * top_k <= 2^30; 0 <= n_rows <= 2^30
  * (T * top_k serves every routing; fewer where the caller knows that no more
  * routes are kept).

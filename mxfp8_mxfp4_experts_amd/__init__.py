@@ -12,7 +12,8 @@ integers; ``MoEBlock`` runs them with a ``MoELayer`` as one MoE block.
 
 Beside these there are products in E4M3 with a float scale per block of 128
 (dense, and grouped by expert), and the way of tokens into expert order and
-back with its gradients.
+back with its gradients.  None of the calls is recorded by autograd, whether or
+not its tensors require a gradient: the gradients are calls of their own.
 """
 from ._binding import (  # noqa: F401
     COMBINE_ATOMIC,

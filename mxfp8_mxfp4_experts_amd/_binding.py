@@ -848,7 +848,8 @@ def moe_route_groups(logits, bias, top_k: int, n_group: int = 1, topk_group: int
 
 # ---------------------------------------------------------------------------
 # Products in E4M3 with a float scale for each block of 128.  Codes are uint8 or
-# torch.float8_e4m3fn tensors.
+# torch.float8_e4m3fn tensors.  Autograd records none of these: the gradient in the tokens is the
+# same call with the weight and its scales transposed.
 
 _FP8 = torch.float8_e4m3fn
 
@@ -1086,8 +1087,9 @@ def _tokens_of(route_row, top_k):
 def moe_sort_tokens(x, route_row, top_k: int, rows=None):
     """rows[route_row[t, k]] = x[t] for every kept route: x [T, H] bf16 or
     float32, route_row int32 [T * top_k] of moe_permute, rows [n, H] (n = T *
-    top_k where not given, and rows that no route has hold anything then).  Its
-    gradient is ``moe_unsort_tokens(drows, route_row, None, top_k)``."""
+    top_k where not given, and rows that no route has hold anything then).  Not
+    recorded by autograd: its gradient is ``moe_unsort_tokens(drows, route_row,
+    None, top_k)``."""
     if rows is not None:
         st = _call.sort_tokens((_lib or lib()).at["sort_tokens"], _raw_stream, x, route_row, top_k,
                                rows)
@@ -1116,7 +1118,8 @@ def moe_sort_tokens(x, route_row, top_k: int, rows=None):
 def moe_unsort_tokens(rows, route_row, topk_w, top_k: int, out=None):
     """out[t] = sum over kept k of topk_w[t, k] * rows[route_row[t, k]]: rows
     [n, H] bf16 or float32, topk_w float [T, top_k] or None (the plain sum),
-    out [T, H] of the rows' type."""
+    out [T, H] of the rows' type.  Not recorded by autograd: its gradients are
+    ``moe_unsort_tokens_grad``, or ``moe_sort_tokens`` of the plain sum."""
     if out is not None:
         st = _call.unsort_tokens((_lib or lib()).at["unsort_tokens"], _raw_stream, rows, route_row,
                                  topk_w, top_k, out)

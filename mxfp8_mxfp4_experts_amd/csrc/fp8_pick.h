@@ -130,7 +130,9 @@ inline int64_t fp8_grouped_blocks(int bm, int bn, int R, int E, int N) {
 }
 
 // Grouped: the rows of each expert are known on the GPU only, so as if the R routes were spread
-// evenly over the experts, with half a tile to spare for each.  (Rows by the thousand million are
+// evenly over the experts, with half a tile to spare for each: routes that are dropped count too.
+// (28 experts, 3584 x 3584, 4096 routes of which 1020 are kept: 88.6 us in the 256 x 256 tiles taken,
+// 78.9 in 64 x 128; 8192 of which 2087: 95.0, and 94.2 in 128 x 128; the weights alone take 72.)  (Rows by the thousand million are
 // too many for a launch of small tiles.)
 inline int fp8_pick_grouped(int R, int E, int N, int K) {
   const int stages = (K + 127) / 128, used = E < R ? E : R;

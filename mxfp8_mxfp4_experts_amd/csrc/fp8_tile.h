@@ -21,9 +21,10 @@
 // Rows past the tile's last, chunks past K and stages past the last are loads beyond the buffer's
 // end: they bring zeros and touch no memory.
 //
-// What bounds it: 8192 x 3584 x 7168 in 256 x 256 tiles 172 .. 180 us, 2.4 POP/s, the matrix unit
-// (219 us with 128 x 128 tiles, 330 with 64 x 64); 256 x 3584 x 7168 in 64 x 64 tiles 17 us, 205 MB
-// from the L2s to the CUs at 60 .. 70 bytes/ns per CU (18.9 with 64 x 128 tiles and K in two).
+// What bounds it (back to back in a graph; a traced dispatch reads up to 10% longer): 8192 x 3584 x
+// 7168 in 256 x 256 tiles 178 .. 189 us, 2.2 .. 2.4 POP/s, the matrix unit (224 us with 128 x 128
+// tiles, 340 with 64 x 64); 256 x 3584 x 7168 in 64 x 64 tiles 17.7 us, 205 MB from the L2s to the CUs
+// at 60 .. 70 bytes/ns per CU (19.1 with 64 x 128 tiles and K in two, 21.3 with 128 x 128 in four).
 // Deeper rings, two stages per barrier, weights laid out by K and prefetches into L2 gained
 // nothing; with 224 columns a tile, a wavefront's columns meet two scales and each product needs
 // a multiplication more, which took what the better fit of 3584 columns gave.
@@ -639,9 +640,9 @@ __device__ __forceinline__ Fp8Found fp8_find(const Fp8Params& p, int per, Fp8Cou
 // Grouped: a workgroup for every tile that there can be; it counts the experts' tiles to find its
 // own, or that there is none left for it.  Each XCD takes a contiguous range of the tiles, an
 // expert's column by column, so that what runs at once on an XCD shares weights and tokens.
-// (Workgroups that stay and take tile after tile were slower: 16384 x 3584 x 3584 in 32 experts
-// 316 us against 278: nothing covers a tile's first loads and its stores.  All experts' whole tiles
-// first and the last, shorter ones of each after them: in 28 experts 269 against 241, since an
+// (Workgroups that stay and take tile after tile were slower, in an earlier form of this kernel: 16384
+// x 3584 x 3584 in 32 experts 316 us against 278, in 28 359 against 288: nothing covers a tile's first
+// loads and its stores.  All experts' whole tiles first and the last, shorter ones of each after them: in 28 experts 269 against 241, since an
 // expert's tiles then no longer share its weights.)
 template <int WM, int WN, int MI, int NI, int NBUF>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
