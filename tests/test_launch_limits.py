@@ -32,6 +32,14 @@ def m():
     return mod
 
 
+@pytest.fixture(autouse=True)
+def memory_given_back():
+    """These tests take up to 200 GiB."""
+    yield
+    if torch.cuda.is_available():
+        torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("threads", [64, 256, 512, 1024])
 def test_a_launch_stays_below_its_limit(probe, threads):
     most = probe.probe_most_blocks(threads)
